@@ -1,6 +1,8 @@
 /*
  * q4moe.h -- C ABI of the MI355X (gfx950) Q4/Q8 expert library: gate/up +
- * SwiGLU, the down projection and the whole expert, over expert slots.
+ * SwiGLU, the down projection and the whole expert, over expert slots, and the
+ * layer around them: a group-scaled 4-bit linear, the router with its balance
+ * loss, and the combination of the expert outputs.
  *
  * What is computed (diff of @mlx-bun/inference 1.0.0, page 52,
  * kernels/glm52/streamed-experts.ts, GATE_UP_SOURCE and its launch in
@@ -501,6 +503,154 @@ int q8_validate_down_grouped_f32(const void *slots_base, uint64_t slot_stride,
                                  int64_t I, const void *out_f32, const void *workspace,
                                  size_t workspace_bytes);
 
+/*
+ * The layer around the experts.  The calls below turn a token's hidden state
+ * into the slot ids the grouped calls read and their outputs back into one
+ * row: a linear with group-scaled 4-bit weights, the router with its balance
+ * loss, and the weighted combination of the expert outputs; the last two with
+ * their gradients.  Conventions as above (borrowed device pointers,
+ * asynchronous, validated on the host, no device memory allocated, no
+ * synchronisation, results the same on every run).  Every tensor is contiguous.
+ * The names without suffix take and give bf16 rows, those with _f32 float32.
+ */
+
+/* Types of the group scales and biases of q4_linear. */
+enum { Q4_SCALE_BF16 = 0, Q4_SCALE_F32 = 1 };
+
+/*
+ * Linear with 4-bit weights and a scale for each group of a row:
+ *
+ *   out[m,n] = sum_k W[n,k] * x[m,k]
+ *   W[n,k] = scales[n, k / group] * (q[n,k] - 8)                  (biases NULL)
+ *   W[n,k] = scales[n, k / group] * q[n,k] + biases[n, k / group]
+ *
+ * q[n,k] is nibble (k % 8) of the little-endian uint32 word (n*K/8 + k/8), the
+ * packing of the expert slots.  Sums are F32 (each group's sum of integer
+ * multiples of x, then its scale), rounded once to the output's type.  The
+ * result of a token does not depend on the other tokens of the call or their
+ * number.
+ *   weights  device, K/2 bytes a row, N rows, 16-byte aligned.
+ *   scales, biases  device, [N][ceil(K/group)], bf16 or F32 by scale_type,
+ *            aligned to their type; the last group of a row may be short.
+ *   group    32, 64 or 128.
+ *   x        device, [M][K], 16-byte aligned; out device, [M][N], aligned to its type.
+ * Limits: 1 <= M <= 65535, 8 <= K <= 65536 with K % 8 == 0, 1 <= N,
+ * N*K/2 <= 2^31 - 16.
+ */
+int q4_linear(const void *weights, const void *scales, const void *biases, int scale_type,
+              int64_t group, const void *x_bf16, int64_t M, int64_t N, int64_t K,
+              void *out_bf16, q4_stream_t stream);
+int q4_linear_f32(const void *weights, const void *scales, const void *biases, int scale_type,
+                  int64_t group, const void *x_f32, int64_t M, int64_t N, int64_t K,
+                  void *out_f32, q4_stream_t stream);
+int q4_validate_linear(const void *weights, const void *scales, const void *biases, int scale_type,
+                       int64_t group, const void *x_bf16, int64_t M, int64_t N, int64_t K,
+                       const void *out_bf16);
+int q4_validate_linear_f32(const void *weights, const void *scales, const void *biases,
+                           int scale_type, int64_t group, const void *x_f32, int64_t M, int64_t N,
+                           int64_t K, const void *out_f32);
+
+/* Router scores: softmax over the experts, or the sigmoid of each logit. */
+enum { Q4_SCORE_SOFTMAX = 0, Q4_SCORE_SIGMOID = 1 };
+
+/*
+ * Router.  For each token t with logits l[E]:
+ *   score_e = softmax(l)_e            or  1 / (1 + exp(-l_e))
+ *   ids     = the K experts of highest l_e, or of highest score_e + select_bias_e
+ *             when select_bias is given, best first, ties to the lowest index;
+ *   w_j     = scale * score_{ids_j}, divided by the sum of the chosen scores
+ *             when renormalize != 0 (0 when that sum is 0).
+ * An expert whose logit (or bias) is -inf is never chosen: places left over
+ * hold id -1 and weight 0, which the grouped calls answer with zero rows and
+ * q4_combine skips.  A token whose mask byte is 0, or whose logits are all
+ * -inf, has -1 in every place and counts nowhere below; nothing of its logits
+ * reaches a result.  A NaN logit ranks above every number and makes the
+ * token's softmax weights NaN.  With select_bias the order is that of
+ * the sums in double precision.
+ *
+ * Batch statistics, each written when its pointer is given (T tokens counted):
+ *   counts[e]    = number of (token, place) pairs that chose e          (int32)
+ *   loss         = E * sum_e (counts[e] / (K T)) * (1/T) sum_t p[t,e]   (F32)
+ *   loss_grad[e] = d loss / d p[t,e] = E * counts[e] / (K T^2)          (F32)
+ * p[t] is the score over its sum (softmax: the score).  T = 0 gives zeros.
+ *   select_bias  device F32 [E] or NULL; token_mask device uint8 [M] or NULL.
+ *   ids          device int32 [M][K]; weights device F32 [M][K].
+ *   workspace    device, 256-byte aligned, q4_route_workspace_bytes(M, E)
+ *                bytes; may be NULL when counts, loss and loss_grad are.
+ * Limits: 1 <= M <= 2^24, 1 <= E <= 1024, 1 <= K <= min(E, 64).
+ */
+size_t q4_route_workspace_bytes(int64_t M, int64_t E);
+int q4_route(const void *logits_bf16, int64_t M, int64_t E, int64_t K, int score, int renormalize,
+             float scale, const float *select_bias, const uint8_t *token_mask, int32_t *ids,
+             float *weights, int32_t *counts, float *loss, float *loss_grad, void *workspace,
+             size_t workspace_bytes, q4_stream_t stream);
+int q4_route_f32(const void *logits_f32, int64_t M, int64_t E, int64_t K, int score,
+                 int renormalize, float scale, const float *select_bias, const uint8_t *token_mask,
+                 int32_t *ids, float *weights, int32_t *counts, float *loss, float *loss_grad,
+                 void *workspace, size_t workspace_bytes, q4_stream_t stream);
+
+/*
+ * Gradient of the logits (their type): from d_weights [M][K], the gradient of
+ * the weights, and d_loss [1] (device F32), the gradient of the balance loss,
+ * whose loss_grad [E] the forward call wrote.  Either may be NULL (d_loss and
+ * loss_grad go together).  ids are those of the forward call, score,
+ * renormalize and scale its arguments; a token whose ids[t][0] is negative
+ * gets zeros, ids outside [0, E) nothing.  The choice itself and select_bias
+ * have no gradient.
+ */
+int q4_route_backward(const void *logits_bf16, int64_t M, int64_t E, int64_t K, int score,
+                      int renormalize, float scale, const int32_t *ids, const float *d_weights,
+                      const float *d_loss, const float *loss_grad, void *d_logits_bf16,
+                      q4_stream_t stream);
+int q4_route_backward_f32(const void *logits_f32, int64_t M, int64_t E, int64_t K, int score,
+                          int renormalize, float scale, const int32_t *ids, const float *d_weights,
+                          const float *d_loss, const float *loss_grad, void *d_logits_f32,
+                          q4_stream_t stream);
+int q4_validate_route(const void *logits, int64_t M, int64_t E, int64_t K, int score,
+                      const float *select_bias, const uint8_t *token_mask, const int32_t *ids,
+                      const float *weights, const int32_t *counts, const float *loss,
+                      const float *loss_grad, const void *workspace, size_t workspace_bytes);
+int q4_validate_route_backward(const void *logits, int64_t M, int64_t E, int64_t K, int score,
+                               const int32_t *ids, const float *d_weights, const float *d_loss,
+                               const float *loss_grad, const void *d_logits);
+
+/*
+ * Combination of the expert outputs q4_expert_forward_grouped writes:
+ *   out[t,:] = base[t,:] + sum_j weights[t,j] * y[t,j,:]
+ * summed in F32 over j in order, rounded once.  y [M][K][H], weights F32
+ * [M][K], base and out [M][H]; base may be NULL (zero) and may be out itself.
+ *   slot_ids  int32 [M][K] or NULL.  A pair whose id is outside [0, num_slots)
+ *             is left out, and its row of y is not read.
+ * y, base and out are 16-byte aligned.  Limits: M >= 1, K >= 1,
+ * M*K <= 2^31 - 1, 8 <= H <= 65536 with H % 8 == 0, num_slots >= 1 with slot_ids.
+ */
+int q4_combine(const void *y_bf16, const float *weights, const int32_t *slot_ids,
+               int64_t num_slots, const void *base_bf16, int64_t M, int64_t K, int64_t H,
+               void *out_bf16, q4_stream_t stream);
+int q4_combine_f32(const void *y_f32, const float *weights, const int32_t *slot_ids,
+                   int64_t num_slots, const void *base_f32, int64_t M, int64_t K, int64_t H,
+                   void *out_f32, q4_stream_t stream);
+
+/*
+ * Gradients of q4_combine from d_out [M][H]:
+ *   d_y[t,j,:]     = weights[t,j] * d_out[t,:]               (the type of y)
+ *   d_weights[t,j] = sum_h d_out[t,h] * y[t,j,h]             (F32)
+ * zero for a pair that was left out; base's gradient is d_out.  d_y or
+ * d_weights may be NULL (not both); y may be NULL when d_weights is.
+ */
+int q4_combine_backward(const void *d_out_bf16, const void *y_bf16, const float *weights,
+                        const int32_t *slot_ids, int64_t num_slots, int64_t M, int64_t K, int64_t H,
+                        void *d_y_bf16, float *d_weights, q4_stream_t stream);
+int q4_combine_backward_f32(const void *d_out_f32, const void *y_f32, const float *weights,
+                            const int32_t *slot_ids, int64_t num_slots, int64_t M, int64_t K,
+                            int64_t H, void *d_y_f32, float *d_weights, q4_stream_t stream);
+int q4_validate_combine(const void *y, const float *weights, const int32_t *slot_ids,
+                        int64_t num_slots, const void *base, int64_t M, int64_t K, int64_t H,
+                        const void *out);
+int q4_validate_combine_backward(const void *d_out, const void *y, const float *weights,
+                                 const int32_t *slot_ids, int64_t num_slots, int64_t M, int64_t K,
+                                 int64_t H, const void *d_y, const float *d_weights);
+
 /* Message for the last failing call on this thread ("" after success). */
 const char *q4_last_error(void);
 
@@ -532,7 +682,8 @@ int q4_stream_read(const void *slots_base, uint64_t slot_stride, int64_t num_slo
 
 /* ABI version: 5 (1 plus the down projection and whole-expert calls, the Q8
  * family, f32 activations, the (M, K, num_slots) workspace query and the
- * streaming-read measurement aid). */
+ * streaming-read measurement aid).  Calls added without a change to an earlier
+ * one (the layer's) leave it as it is. */
 int q4_abi_version(void);
 
 #ifdef __cplusplus

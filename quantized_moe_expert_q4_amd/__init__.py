@@ -1,4 +1,6 @@
-"""MI355X-native Q4 expert: gate/up + SwiGLU, down projection, whole expert.
+"""MI355X-native Q4 expert: gate/up + SwiGLU, down projection, whole expert, and
+the layer around it: group-scaled 4-bit linear, router with its balance loss,
+combination of the expert outputs.
 
 The computation lives in hand-written HIP kernels for gfx950 behind the C ABI
 of ``include/q4moe.h`` (``libq4moe.so`` in this package directory).  This
@@ -32,4 +34,15 @@ from ._lib import (  # noqa: F401
     validate_down,
     validate_down_grouped,
     stream_read,
+    linear,
+    route,
+    route_backward,
+    route_workspace_bytes,
+    combine,
+    combine_backward,
+    validate_linear,
+    validate_route,
+    validate_route_backward,
+    validate_combine,
+    validate_combine_backward,
 )

@@ -154,6 +154,20 @@ _SIGNATURES = {
     "q8_validate_down_grouped_f32": (ctypes.c_int, [_P, _U64, _I64, _LAYOUT, _P, _I64, _P, _I64, _I64, _I64, _P,
                                                 _P, _SZ]),
 }
+_INT, _F32 = ctypes.c_int, ctypes.c_float
+for _suffix in ("", "_f32"):
+    _SIGNATURES["q4_linear" + _suffix] = (_INT, [_P, _P, _P, _INT, _I64, _P, _I64, _I64, _I64, _P, _P])
+    _SIGNATURES["q4_validate_linear" + _suffix] = (_INT, [_P, _P, _P, _INT, _I64, _P, _I64, _I64, _I64, _P])
+    _SIGNATURES["q4_route" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                _SZ, _P])
+    _SIGNATURES["q4_route_backward" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P])
+    _SIGNATURES["q4_combine" + _suffix] = (_INT, [_P, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P])
+    _SIGNATURES["q4_combine_backward" + _suffix] = (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P])
+_SIGNATURES["q4_route_workspace_bytes"] = (_SZ, [_I64, _I64])
+_SIGNATURES["q4_validate_route"] = (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _SZ])
+_SIGNATURES["q4_validate_route_backward"] = (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P])
+_SIGNATURES["q4_validate_combine"] = (_INT, [_P, _P, _P, _I64, _P, _I64, _I64, _I64, _P])
+_SIGNATURES["q4_validate_combine_backward"] = (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P])
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -417,3 +431,132 @@ def stream_read(slots_base, slot_stride: int, num_slots: int, offset_a: int, off
           ("sink", sink, "int32", 1))
     _check(load().q4_stream_read(_ptr(slots_base), slot_stride, num_slots, offset_a, offset_b, rows, row_bytes,
                                  pattern, waves, depth, _ptr(sink), _stream(stream)))
+
+
+# ---- the layer around the experts: linear, router, combination ----
+
+_SCALE_TYPES = {"bfloat16": 0, "float32": 1}     # Q4_SCALE_BF16, Q4_SCALE_F32
+_SCORES = {"softmax": 0, "sigmoid": 1}           # Q4_SCORE_SOFTMAX, Q4_SCORE_SIGMOID
+
+
+def _scale_type(scales, scale_dtype: Optional[str]) -> str:
+    """Type of the group scales: that of the tensor, or ``scale_dtype`` for a raw pointer."""
+    if scales is None or isinstance(scales, int):
+        return scale_dtype or "bfloat16"
+    got = str(scales.dtype).replace("torch.", "")
+    if got not in _SCALE_TYPES:
+        raise ValueError(f"scales must be a bfloat16 or float32 tensor, not {got}")
+    return got
+
+
+def _score(score: str) -> int:
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', not {score!r}")
+    return _SCORES[score]
+
+
+def linear(weights, scales, x, M: int, N: int, K: int, group: int, out, biases=None, stream=None,
+           xdtype: str = "bf16", scale_dtype: Optional[str] = None) -> None:
+    """Enqueue the group-scaled 4-bit linear (see q4_linear in include/q4moe.h).
+
+    ``weights`` uint8 [N, K/2], ``scales`` and ``biases`` [N, ceil(K/group)]
+    in bf16 or F32, ``x`` [M, K] and ``out`` [M, N] in ``xdtype``."""
+    fn = _fn(load(), "q4", "linear", xdtype)
+    xt = _XDTYPE_NAMES[xdtype]
+    st = _scale_type(scales, scale_dtype)
+    n_scales = N * -(-K // group) if group in (32, 64, 128) else 0     # other groups: the library refuses the call
+    _args(("weights", weights, "uint8", N * (K // 2)), ("scales", scales, st, n_scales),
+          ("biases", biases, st, n_scales), ("x", x, xt, M * K), ("out", out, xt, M * N))
+    _check(fn(_ptr(weights), _ptr(scales), _ptr(biases), _SCALE_TYPES[st], group, _ptr(x), M, N, K, _ptr(out),
+              _stream(stream)))
+
+
+def validate_linear(weights, scales, x, M: int, N: int, K: int, group: int, out, biases=None, xdtype: str = "bf16",
+                    scale_dtype: Optional[str] = None) -> int:
+    """Host-only argument check of the linear; returns the status."""
+    return _fn(load(), "q4", "validate_linear", xdtype)(
+        _ptr(weights), _ptr(scales), _ptr(biases), _SCALE_TYPES[_scale_type(scales, scale_dtype)], group, _ptr(x), M, N, K,
+        _ptr(out))
+
+
+def route_workspace_bytes(M: int, E: int) -> int:
+    return int(load().q4_route_workspace_bytes(M, E))
+
+
+def route(logits, M: int, E: int, K: int, ids, weights, score: str = "softmax", renormalize: bool = False,
+          scale: float = 1.0, select_bias=None, token_mask=None, counts=None, loss=None, loss_grad=None,
+          workspace=None, workspace_bytes: int = 0, stream=None, xdtype: str = "bf16") -> None:
+    """Enqueue the router (see q4_route in include/q4moe.h): ``ids`` int32 and
+    ``weights`` F32 [M, K] from ``logits`` [M, E] in ``xdtype``; ``counts``
+    (int32 [E]), ``loss`` (F32 [1]) and ``loss_grad`` (F32 [E]) when given."""
+    fn = _fn(load(), "q4", "route", xdtype)
+    _args(("logits", logits, _XDTYPE_NAMES[xdtype], M * E), ("ids", ids, "int32", M * K),
+          ("weights", weights, "float32", M * K), ("select_bias", select_bias, "float32", E),
+          ("token_mask", token_mask, "uint8", M), ("counts", counts, "int32", E), ("loss", loss, "float32", 1),
+          ("loss_grad", loss_grad, "float32", E), ("workspace", workspace, "uint8", workspace_bytes))
+    _check(fn(_ptr(logits), M, E, K, _score(score), int(renormalize), scale, _ptr(select_bias), _ptr(token_mask),
+              _ptr(ids), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(workspace), workspace_bytes,
+              _stream(stream)))
+
+
+def validate_route(logits, M: int, E: int, K: int, ids, weights, score: str = "softmax", select_bias=None,
+                   token_mask=None, counts=None, loss=None, loss_grad=None, workspace=None,
+                   workspace_bytes: int = 0) -> int:
+    """Host-only argument check of the router; returns the status."""
+    return load().q4_validate_route(_ptr(logits), M, E, K, _score(score), _ptr(select_bias), _ptr(token_mask), _ptr(ids),
+                                    _ptr(weights), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(workspace),
+                                    workspace_bytes)
+
+
+def route_backward(logits, M: int, E: int, K: int, ids, d_logits, d_weights=None, d_loss=None, loss_grad=None,
+                   score: str = "softmax", renormalize: bool = False, scale: float = 1.0, stream=None,
+                   xdtype: str = "bf16") -> None:
+    """Enqueue the gradient of the router's logits (see q4_route_backward in include/q4moe.h)."""
+    fn = _fn(load(), "q4", "route_backward", xdtype)
+    xt = _XDTYPE_NAMES[xdtype]
+    _args(("logits", logits, xt, M * E), ("ids", ids, "int32", M * K), ("d_weights", d_weights, "float32", M * K),
+          ("d_loss", d_loss, "float32", 1), ("loss_grad", loss_grad, "float32", E), ("d_logits", d_logits, xt, M * E))
+    _check(fn(_ptr(logits), M, E, K, _score(score), int(renormalize), scale, _ptr(ids), _ptr(d_weights), _ptr(d_loss),
+              _ptr(loss_grad), _ptr(d_logits), _stream(stream)))
+
+
+def validate_route_backward(logits, M: int, E: int, K: int, ids, d_logits, d_weights=None, d_loss=None,
+                            loss_grad=None, score: str = "softmax") -> int:
+    """Host-only argument check of the router's gradient; returns the status."""
+    return load().q4_validate_route_backward(_ptr(logits), M, E, K, _score(score), _ptr(ids), _ptr(d_weights),
+                                             _ptr(d_loss), _ptr(loss_grad), _ptr(d_logits))
+
+
+def combine(y, weights, M: int, K: int, H: int, out, slot_ids=None, num_slots: int = 0, base=None, stream=None,
+            xdtype: str = "bf16") -> None:
+    """Enqueue the weighted combination of expert outputs (see q4_combine in
+    include/q4moe.h): ``y`` [M, K, H] with F32 ``weights`` [M, K] onto ``base``."""
+    fn = _fn(load(), "q4", "combine", xdtype)
+    xt = _XDTYPE_NAMES[xdtype]
+    _args(("y", y, xt, M * K * H), ("weights", weights, "float32", M * K), ("slot_ids", slot_ids, "int32", M * K),
+          ("base", base, xt, M * H), ("out", out, xt, M * H))
+    _check(fn(_ptr(y), _ptr(weights), _ptr(slot_ids), num_slots, _ptr(base), M, K, H, _ptr(out), _stream(stream)))
+
+
+def validate_combine(y, weights, M: int, K: int, H: int, out, slot_ids=None, num_slots: int = 0, base=None) -> int:
+    """Host-only argument check of the combination; returns the status."""
+    return load().q4_validate_combine(_ptr(y), _ptr(weights), _ptr(slot_ids), num_slots, _ptr(base), M, K, H, _ptr(out))
+
+
+def combine_backward(d_out, y, weights, M: int, K: int, H: int, d_y=None, d_weights=None, slot_ids=None,
+                     num_slots: int = 0, stream=None, xdtype: str = "bf16") -> None:
+    """Enqueue the gradients of the combination (see q4_combine_backward in include/q4moe.h)."""
+    fn = _fn(load(), "q4", "combine_backward", xdtype)
+    xt = _XDTYPE_NAMES[xdtype]
+    _args(("d_out", d_out, xt, M * H), ("y", y, xt, M * K * H), ("weights", weights, "float32", M * K),
+          ("slot_ids", slot_ids, "int32", M * K), ("d_y", d_y, xt, M * K * H),
+          ("d_weights", d_weights, "float32", M * K))
+    _check(fn(_ptr(d_out), _ptr(y), _ptr(weights), _ptr(slot_ids), num_slots, M, K, H, _ptr(d_y), _ptr(d_weights),
+              _stream(stream)))
+
+
+def validate_combine_backward(d_out, y, weights, M: int, K: int, H: int, d_y=None, d_weights=None, slot_ids=None,
+                              num_slots: int = 0) -> int:
+    """Host-only argument check of the combination's gradients; returns the status."""
+    return load().q4_validate_combine_backward(_ptr(d_out), _ptr(y), _ptr(weights), _ptr(slot_ids), num_slots, M, K, H,
+                                               _ptr(d_y), _ptr(d_weights))

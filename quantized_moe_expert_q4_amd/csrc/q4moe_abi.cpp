@@ -15,6 +15,7 @@
 #include <string>
 
 #include "q4moe.h"
+#include "q4moe_error.h"
 #include "q4moe_launch.h"
 #include "q4moe_stream.h"
 
@@ -264,6 +265,16 @@ int run_down_grouped(unsigned fmt, const void* base, uint64_t stride, int64_t nu
 }
 
 }  // namespace
+
+// a message that cannot be stored is dropped: no exception leaves a C entry
+int q4::report(int code, const char* msg) noexcept {
+  try {
+    g_err = msg;
+  } catch (...) {
+    g_err.clear();
+  }
+  return code;
+}
 
 extern "C" {
 
