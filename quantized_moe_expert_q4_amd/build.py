@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libq4moe.so")
 
 SOURCES = ["q4moe_resident.hip", "q4moe_batch.hip", "q4moe_chunked.hip", "q4moe_stream.hip", "q4moe_sigmoid.hip", "q4moe_noalloc.hip",
-           "q4moe_linear.hip", "q4moe_route.hip", "q4moe_combine.hip", "q4moe_abi.cpp", "q4moe_layer_abi.cpp"]
+           "q4moe_linear.hip", "q4moe_linear32.hip", "q4moe_linear64.hip", "q4moe_linear128.hip",
+           "q4moe_route.hip", "q4moe_combine.hip", "q4moe_abi.cpp", "q4moe_layer_abi.cpp"]
 
 FLAGS = [
     "--offload-arch=gfx950",
