@@ -170,6 +170,7 @@ _SIGNATURES["q4_validate_combine"] = (_INT, [_P, _P, _P, _I64, _P, _I64, _I64, _
 _SIGNATURES["q4_validate_combine_backward"] = (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P])
 
 _lib: Optional[ctypes.CDLL] = None
+_fns: dict = {}                 # entry points by (weight format, name, activation dtype)
 
 
 def load() -> ctypes.CDLL:
@@ -194,11 +195,15 @@ def _fn(lib, fmt: str, name: str, xdtype: str = "bf16"):
     """Entry point ``<fmt>_<name>[_f32]`` of the library: ``fmt`` is "q4"
     (packed nibbles) or "q8" (int8 weights); ``xdtype`` is "bf16" or "f32"
     (activations and outputs)."""
+    fn = _fns.get((fmt, name, xdtype))
+    if fn is not None:
+        return fn
     if fmt not in ("q4", "q8"):
         raise ValueError(f"weight format must be 'q4' or 'q8', not {fmt!r}")
     if xdtype not in ("bf16", "f32"):
         raise ValueError(f"activation dtype must be 'bf16' or 'f32', not {xdtype!r}")
-    return getattr(lib, f"{fmt}_{name}" + ("_f32" if xdtype == "f32" else ""))
+    fn = _fns[fmt, name, xdtype] = getattr(lib, f"{fmt}_{name}" + ("_f32" if xdtype == "f32" else ""))
+    return fn
 
 
 def last_error() -> str:
@@ -234,11 +239,33 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """Handle of the current device's current stream, without a Stream object
+    where torch offers it (the object costs a small call a quarter of its time)."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", False)
+    if not _raw_stream:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
+
+
+_raw_stream = None
+_dtype_names: dict = {}         # torch dtype -> its name
+
+
+def _dtype_name(dtype) -> str:
+    name = _dtype_names.get(dtype)
+    if name is None:
+        name = _dtype_names[dtype] = str(dtype).replace("torch.", "")
+    return name
 
 
 _XDTYPE_NAMES = {"bf16": "bfloat16", "f32": "float32"}
@@ -251,9 +278,15 @@ def _args(*specs) -> None:
     (dtype, layout and size of every argument are checked before any
     device).  Raw integer pointers pass unchecked; None is left to the
     library's own checks (required pointers) or means "skip" (probes)."""
+    for name, t, dtype, numel in specs:
+        if t is not None and not isinstance(t, int) and not (
+                _dtype_name(t.dtype) == dtype and t.numel() >= numel and t.is_cuda and t.is_contiguous()):
+            break
+    else:
+        return
     live = [sp for sp in specs if sp[1] is not None and not isinstance(sp[1], int)]
     for name, t, dtype, numel in live:
-        got = str(t.dtype).replace("torch.", "")
+        got = _dtype_name(t.dtype)
         if got != dtype:
             raise ValueError(f"{name} must be a {dtype} tensor, not {got}")
         if not t.is_contiguous():
@@ -443,7 +476,7 @@ def _scale_type(scales, scale_dtype: Optional[str]) -> str:
     """Type of the group scales: that of the tensor, or ``scale_dtype`` for a raw pointer."""
     if scales is None or isinstance(scales, int):
         return scale_dtype or "bfloat16"
-    got = str(scales.dtype).replace("torch.", "")
+    got = _dtype_name(scales.dtype)
     if got not in _SCALE_TYPES:
         raise ValueError(f"scales must be a bfloat16 or float32 tensor, not {got}")
     return got
