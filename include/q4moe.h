@@ -562,8 +562,8 @@ enum { Q4_SCORE_SOFTMAX = 0, Q4_SCORE_SIGMOID = 1 };
  *             when renormalize != 0 (0 when that sum is 0).
  * An expert whose logit (or bias) is -inf is never chosen: places left over
  * hold id -1 and weight 0, which the grouped calls answer with zero rows and
- * q4_combine skips.  A token whose mask byte is 0, or whose logits are all
- * -inf, has -1 in every place and counts nowhere below; nothing of its logits
+ * q4_combine skips.  A token whose mask byte is 0, or that can choose no expert,
+ * has -1 in every place and counts nowhere below; nothing of its logits
  * reaches a result.  A NaN logit ranks above every number and makes the
  * token's softmax weights NaN.  With select_bias the order is that of
  * the sums in double precision.
