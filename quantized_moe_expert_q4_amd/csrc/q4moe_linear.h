@@ -121,12 +121,6 @@ __device__ __forceinline__ void read_scales(const uint8_t* at, float (&f)[COUNT]
 
 constexpr int kLinearWaves = 8;
 
-// Waves along K: as the launch chooses (0), or fixed, so that a step's staged
-// tokens, 64 KB (float: 96 KB) at most, are fetched into a fixed number of
-// registers while the step before is at work.
-template <bool XF, int TK>
-constexpr int kLinearSplit = TK <= 4 ? 0 : TK * (XF ? 2 : 1) >= 64 ? 2 : TK * (XF ? 2 : 1) >= (XF ? 16 : 32) ? 4 : 8;
-
 // Weights of a wave in flight, in units; a chunk has as many steps.
 template <bool XF, int TK>
 constexpr int kLinearRing = TK * (XF ? 3 : 1) <= 4 ? 2 : 1;
@@ -151,9 +145,12 @@ struct LinearPlan {
 
 // KPG: 32-weight blocks of a group (1, 2, 4).  TK: tokens of the work-group at
 // most; up to four keep one sum a lane (matrix row 4 t + i holds token t).  T:
-// row tiles of a wave.
-template <int KPG, bool AFF, bool SF, bool XF, int TK, int T>
-__global__ __launch_bounds__(kLinearWaves * 64, TK <= 16 ? 4 : 2) void linear_kernel(LinearParams p, LinearPlan plan) {
+// row tiles of a wave.  kSplit: waves along K, as the launch chooses (0, up to
+// four tokens) or fixed, so that a step's staged tokens, 64 KB (float: 96 KB) at
+// most, are fetched into a fixed number of registers while the step before is
+// at work.
+template <int KPG, bool AFF, bool SF, bool XF, int TK, int T, int kSplit>
+__global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) void linear_kernel(LinearParams p, LinearPlan plan) {
   constexpr int kParts = XF ? 3 : 1;
   constexpr int kGroups = 8 / KPG;                 // groups of a unit
   constexpr int MT = TK > 16 ? TK / 16 : 1;        // tiles of 16 tokens
@@ -170,7 +167,6 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= 16 ? 4 : 2) void linear_ke
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, q = lane >> 4;
   const bool high = (lane & 8) != 0;
-  constexpr int kSplit = kLinearSplit<XF, TK>;
   const int S = kSplit ? kSplit : plan.S, shift = kSplit ? __builtin_ctz(kSplit) : plan.shift;
   const int log_chunk = kSplit ? 0 : plan.log_chunk, chunk = 1 << log_chunk;
   const int ks = wave & (S - 1), set = wave >> shift, sets = kLinearWaves >> shift;
@@ -531,7 +527,7 @@ constexpr int kLinearStage = 72 * 1024;
 // Most that it takes.
 constexpr int kLinearLds = 144 * 1024;
 
-template <int KPG, bool AFF, bool SF, bool XF, int TK, int T>
+template <int KPG, bool AFF, bool SF, bool XF, int TK, int T, int kSplit>
 hipError_t linear_launch(const LinearParams& p, int split, hipStream_t stream) {
   constexpr int MT = TK > 16 ? TK / 16 : 1, kGroups = 8 / KPG, kScale = SF ? 4 : 2;
   const int units = (p.K + 255) / 256;
@@ -551,8 +547,8 @@ hipError_t linear_launch(const LinearParams& p, int split, hipStream_t stream) {
     return plan.x_bytes + plan.xs_bytes + (AFF ? 2 : 1) * plan.scale_bytes;
   };
   int log_chunk = kLinearRing<XF, TK> - 1, log_scales = log_chunk, stage;
-  if constexpr (kLinearSplit<XF, TK> != 0) {
-    split = kLinearSplit<XF, TK>;
+  if constexpr (kSplit != 0) {
+    split = kSplit;
     const int at_most = staged(split, 0, 0) < kLinearStage ? kLinearStage : kLinearLds;
     while (staged(split, 0, log_scales + 1) <= at_most && (1 << log_scales) < steps) ++log_scales;
   } else {
@@ -565,7 +561,7 @@ hipError_t linear_launch(const LinearParams& p, int split, hipStream_t stream) {
   const size_t lds = (size_t)(stage > sums ? stage : sums);
   LinearParams q = p;
   void* args[] = {&q, &plan};
-  const void* const f = reinterpret_cast<const void*>(&linear_kernel<KPG, AFF, SF, XF, TK, T>);
+  const void* const f = reinterpret_cast<const void*>(&linear_kernel<KPG, AFF, SF, XF, TK, T, kSplit>);
   return hipLaunchKernel(f, dim3((unsigned)((p.N + 16 * T * sets - 1) / (16 * T * sets)), (unsigned)((p.M + TK - 1) / TK)),
                          dim3(kLinearWaves * 64), args, lds, stream);
 }
@@ -581,33 +577,44 @@ hipError_t linear_tiles(const LinearParams& p, hipStream_t stream) {
     const int units = (p.K + 255) / 256;
     int split = 1;
     while (split < 8 && split * 2 <= units && split * tiles < 2048) split *= 2;
-    return linear_launch<KPG, AFF, SF, XF, TK, 1>(p, split, stream);
+    return linear_launch<KPG, AFF, SF, XF, TK, 1, 0>(p, split, stream);
+  } else if constexpr (TK == 64) {
+    return linear_launch<KPG, AFF, SF, XF, TK, 1, 2>(p, 0, stream);
   } else {
-    // two tiles share the tokens' reads from LDS once there are work-groups
-    // enough (14336 rows of 7168: 16 tokens 28.6 us against 32, 32 tokens 30.9
-    // against 47, 64 float tokens 65 against 90); 64 tokens have registers for one
-    if constexpr (TK < 64) {
-      constexpr int S = kLinearSplit<XF, TK>;
-      if (tiles * S >= (S == 2 ? 1600 : 3000)) return linear_launch<KPG, AFF, SF, XF, TK, 2>(p, 0, stream);
+    constexpr int S = XF && TK == 32 ? 2 : 4;
+    if constexpr (!XF && TK <= 16) {
+      // few rows: all waves along K (16 tokens, 4096 rows of 4096: 8.8 us
+      // against 10.3; 6144 rows: 12.3 us with four against 18.3)
+      if (tiles * 8 < 3000) return linear_launch<KPG, AFF, SF, XF, TK, 1, 8>(p, 0, stream);
     }
-    return linear_launch<KPG, AFF, SF, XF, TK, 1>(p, 0, stream);
+    // two tiles of a wave share the tokens' reads from LDS, once there are more
+    // work-groups than the 256 CUs hold at a time (one each by their LDS or
+    // registers, two of the smaller variants): 32 tokens of 4096 take 14.9 us
+    // against 18.3 with 8192 rows (256 work-groups), 23.6 against 16.4 with 10240
+    const int groups = (tiles * S + kLinearWaves - 1) / kLinearWaves * ((p.M + TK - 1) / TK);
+    constexpr int kAtOnce = 256 * (TK * (XF ? 2 : 1) <= 16 ? 2 : 1);
+    if (groups > kAtOnce) return linear_launch<KPG, AFF, SF, XF, TK, 2, S>(p, 0, stream);
+    return linear_launch<KPG, AFF, SF, XF, TK, 1, S>(p, 0, stream);
   }
 }
 
-// Tokens of a work-group: as many as the call has, but with few rows (too few
-// work-groups) fewer, which splits the tokens over more of them and unpacks the
-// weights for each: 64 tokens of 4096 take 42 us together and 51 in two passes
-// with 14336 rows, 31 and 15 with 4096, 31, 15 and (four passes) 11 with 1536.
+// Tokens of a work-group: as many as the call has; with too few work-groups
+// fewer, which spreads the tokens over more of them and unpacks the weights for
+// each.  64 tokens of 4096 take 42 us together and 51 in two passes with 14336
+// rows (224 work-groups in one pass), 31 and 15 with 4096 (64), 31, 15 and, in
+// four passes, 11 with 1536 (24).
 template <int KPG, bool AFF, bool SF, bool XF>
 hipError_t linear_select(const LinearParams& p, hipStream_t stream) {
+  constexpr int kEnough = 150;
   const int tiles = (p.N + 15) / 16;
+  const auto groups = [&](int tokens, int S) { return tiles * S / kLinearWaves * ((p.M + tokens - 1) / tokens); };
   if (p.M == 1) return linear_tiles<KPG, AFF, SF, XF, 1>(p, stream);
   if (p.M <= 4) return linear_tiles<KPG, AFF, SF, XF, 4>(p, stream);
   if (p.M <= 8) return linear_tiles<KPG, AFF, SF, XF, 8>(p, stream);
   if constexpr (!XF) {
-    if (p.M > 32 && tiles >= 600) return linear_tiles<KPG, AFF, SF, XF, 64>(p, stream);
+    if (p.M > 32 && groups(64, 2) >= kEnough) return linear_tiles<KPG, AFF, SF, XF, 64>(p, stream);
   }
-  if (p.M > 16 && tiles >= 160) return linear_tiles<KPG, AFF, SF, XF, 32>(p, stream);
+  if (p.M > 16 && groups(32, XF ? 2 : 4) >= kEnough) return linear_tiles<KPG, AFF, SF, XF, 32>(p, stream);
   return linear_tiles<KPG, AFF, SF, XF, 16>(p, stream);
 }
 
