@@ -528,7 +528,8 @@ enum { Q4_SCALE_BF16 = 0, Q4_SCALE_F32 = 1 };
  * packing of the expert slots.  Sums are F32 (each group's sum of integer
  * multiples of x, then its scale), rounded once to the output's type.  The
  * result of a token does not depend on the other tokens of the call or their
- * number.
+ * number.  A token that holds an infinity or a NaN, or whose 31 * |x| leave the
+ * F32 range when summed over a group, has results that are not finite.
  *   weights  device, K/2 bytes a row, N rows, 16-byte aligned.
  *   scales, biases  device, [N][ceil(K/group)], bf16 or F32 by scale_type,
  *            aligned to their type; the last group of a row may be short.

@@ -17,7 +17,9 @@
 //   s sum q x + b sum x = s (sum (16 + q) x - 16 sum x) - (b / 16) (-16 sum x)
 // Group sums are scaled in F32 into the running total, so products and the
 // scale are exact up to F32 rounding.  Float activations enter as three bf16
-// parts whose sum is the float (8 bits each), three products per weight.
+// parts whose sum is the float (8 bits each), three products per weight, and
+// meet the exact (q - 8) / 16 (20 operations for 8 weights instead of 8):
+//   16 s sum (q - 8) / 16 x + (b + 8 s) sum x
 //
 // Every variant adds a token's products in the same order (S is a rule on N
 // and K alone), so its result does not depend on the number of tokens.
@@ -82,6 +84,21 @@ __device__ __forceinline__ v4u unpack_word(uint32_t w, uint32_t sixteen) {
   r.y = ((w >> 1) & 0x00780078u) | sixteen;
   r.z = ((w >> 5) & 0x00780078u) | sixteen;
   r.w = ((w >> 9) & 0x00780078u) | sixteen;
+  return r;
+}
+
+// The same as (q - 8) / 16, exactly: float activations, whose results keep all
+// their digits, would lose three bits to the offset of 16 + q.  q ^ 8 is the
+// two's complement of q - 8; the conversion takes the low four bits.
+__device__ __forceinline__ v4u unpack_word_exact(uint32_t w) {
+  w ^= 0x88888888u;
+  v4u r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (4 * i)));
+    const float hi = __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (4 * i + 16)));
+    r[i] = perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+  }
   return r;
 }
 
@@ -186,7 +203,8 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
   uint32_t sixteen = 0x41804180u;
   asm("" : "+v"(sixteen));
 
-  const uint32_t cbits = AFF ? 0xC180C180u : 0xC1C0C1C0u;   // -16 or -24
+  constexpr bool kSums = AFF || !XF;               // the tokens' sums over each group are needed
+  const uint32_t cbits = XF ? 0x3F803F80u : AFF ? 0xC180C180u : 0xC1C0C1C0u;   // 1, -16 or -24
   const v4u offs = {cbits, cbits, cbits, cbits};
 
   // wave k's units are [first(k), first(k + 1))
@@ -336,7 +354,7 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
       for (int d = 0; d < kParts; ++d) sum = mfma_bf16(operand(xu, o + j, d, mt), offs, sum);
     return sum;
   };
-  // -24 (-16) times the tokens' sums over each group, as [slot][group][token]
+  // -24 (-16; 1 for floats) times the tokens' sums over each group, as [slot][group][token]
   auto stage_sums = [&]() {
     for (int i = wave; i < (kGroups * MT) << log_slots; i += kLinearWaves) {
       const int mt = i % MT, g = i / MT % kGroups, slot = i / (MT * kGroups);
@@ -440,7 +458,9 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const float* const at = reinterpret_cast<const float*>(s_sums) + (slot * kGroups + g) * TK;
-        if constexpr (TR == 1) {
+        if constexpr (!kSums) {
+          xsum[mt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        } else if constexpr (TR == 1) {
           const float v = at[q & (TK - 1)];
           xsum[mt] = v4f{v, v, v, v};
         } else {
@@ -451,12 +471,12 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) acc[t][mt] = xsum[mt];
+        for (int mt = 0; mt < MT; ++mt) acc[t][mt] = XF ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : xsum[mt];
 #pragma unroll
       for (int j = 0; j < KPG; ++j) {
         v4u bw[T];
 #pragma unroll
-        for (int t = 0; t < T; ++t) bw[t] = unpack_word(word[t][g * KPG + j], sixteen);
+        for (int t = 0; t < T; ++t) bw[t] = XF ? unpack_word_exact(word[t][g * KPG + j]) : unpack_word(word[t][g * KPG + j], sixteen);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -467,8 +487,11 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
           }
       }
       each([&](int t, int mt, int j) {
-        tot[t][mt][j] = __builtin_fmaf(s[t][g], acc[t][mt][j], tot[t][mt][j]);
-        if constexpr (AFF) tot[t][mt][j] = __builtin_fmaf(-0.0625f * b[t][g], xsum[mt][j], tot[t][mt][j]);
+        tot[t][mt][j] = __builtin_fmaf(XF ? 16.0f * s[t][g] : s[t][g], acc[t][mt][j], tot[t][mt][j]);
+        if constexpr (AFF) {
+          const float b1 = XF ? __builtin_fmaf(8.0f, s[t][g], b[t][g]) : -0.0625f * b[t][g];
+          tot[t][mt][j] = __builtin_fmaf(b1, xsum[mt][j], tot[t][mt][j]);
+        }
       });
     }
   };
@@ -483,8 +506,10 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
       }
       put_step(i);
       __syncthreads();
-      stage_sums();
-      __syncthreads();
+      if constexpr (kSums) {
+        stage_sums();
+        __syncthreads();
+      }
       if constexpr (kSplit != 0) fetch_step(i + 1);
       __builtin_amdgcn_sched_barrier(0);
     }
