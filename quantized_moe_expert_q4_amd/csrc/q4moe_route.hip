@@ -11,7 +11,12 @@
 //
 // These kernels are short enough that fetching their code counts: the loops
 // over a lane's experts have no branches, and the rare choice in double
-// precision is one loop over the tokens that need it, a whole wave for each.
+// precision is one loop over the tokens that need it, a whole wave for each
+// (with both unrolled in place the router below took 25 us).
+//
+// Measured: 8192 tokens, 256 experts, sigmoid and bias, eight chosen, with the
+// statistics 14.8 + 6.8 us, bound by the instructions of the nine rounds (4 MB
+// of logits are 1 us of memory traffic); its gradient 8.8; one token 3.5.
 #include "q4moe_device.h"
 #include "q4moe_layer.h"
 
