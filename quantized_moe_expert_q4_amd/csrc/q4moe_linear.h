@@ -15,8 +15,8 @@
 // 70 us).  Weights go straight to registers, a unit or two ahead.
 //
 // What bounds it (one call, bf16 unless said).  One token: the weight stream,
-// 131072 x 4096 with biases in 51 us (5.6 TB/s; its vector instructions alone
-// take about 39); 14336 x 7168 in 15.4.  Many: 64 tokens of 14336 x 7168 in 41 us,
+// 131072 x 4096 with biases in 50 us (5.7 TB/s; its vector instructions alone
+// take about 39); 14336 x 7168 in 15.  Many: 64 tokens of 14336 x 7168 in 41 us,
 // where a step's vector instructions (3600 cycles a SIMD), LDS reads (2800) and
 // matrix operations (1400) overlap little at two waves a SIMD; 16 tokens 19 us,
 // 64 float tokens 65.  Few rows: steps of about 3 us each, bound by latency.
@@ -359,31 +359,25 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
   auto operand = [&](uint32_t xu, int o, int d, int mt) {   // xu: of the unit
     return *reinterpret_cast<const v4u*>(s_mem + xu + xlane[kSwizzle ? o & 3 : 0] + (o * kParts + d) * kOperandX + mt * 256);
   };
-  auto group_sum = [&](uint32_t xu, int o, int mt) {
-    v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < KPG; ++j)
-#pragma unroll
-      for (int d = 0; d < kParts; ++d) sum = mfma_bf16(operand(xu, o + j, d, mt), offs, sum);
-    return sum;
-  };
-  // -24 (-16; 1 for floats) times the tokens' sums over each group, as [slot][group][token]
+  // -24 (-16; 1 for floats) times the tokens' sums over each group, as
+  // [slot][group][token]; a wave keeps to one group of the unit.
   auto stage_sums = [&]() {
-    for (int i = wave; i < (kGroups * MT) << log_slots; i += kLinearWaves) {
-      const int mt = i % MT, g = i / MT % kGroups, slot = i / (MT * kGroups);
-      const uint32_t xu = (uint32_t)(slot * kUnitX + mt * 256);
-      v4f sum;
-      // a group of 32 or 64 starts at any operand mod 4: the swizzle's part of it is chosen here
-      if (KPG == 4 || !kSwizzle) {
-        sum = group_sum(xu + g * (KPG * kParts * kOperandX), 0, 0);
-      } else {
-        constexpr int kPer = 4 / KPG;
-        const uint32_t at = xu + g / kPer * (4 * kParts * kOperandX);
-        sum = group_sum(at, 0, 0);
+    const int g = wave & (kGroups - 1);
+    uint32_t at[KPG];
 #pragma unroll
-        for (int h = 1; h < kPer; ++h)
-          if (g % kPer == h) sum = group_sum(at, h * KPG, 0);
-      }
+    for (int j = 0; j < KPG; ++j) {
+      const int o = g * KPG + j;
+      at[j] = (uint32_t)(o * (kParts * kOperandX) + (q * TK + (mrow ^ ((4 * o + q) & kSwizzle))) * 16);
+    }
+#pragma unroll 4
+    for (int r = wave / kGroups; r < MT << log_slots; r += kLinearWaves / kGroups) {
+      const int mt = r % MT, slot = r / MT;
+      v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < KPG; ++j)
+#pragma unroll
+        for (int d = 0; d < kParts; ++d)
+          sum = mfma_bf16(*reinterpret_cast<const v4u*>(s_mem + at[j] + slot * kUnitX + mt * 256 + d * kOperandX), offs, sum);
       float* const to = reinterpret_cast<float*>(s_sums) + (slot * kGroups + g) * TK;
       if constexpr (TR == 1) {
         if (n == 0 && q < TK) to[q] = sum[0];
@@ -392,6 +386,7 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
       }
     }
   };
+
   // Running sums of the wave's segment of K (an eighth of the units), and sums
   // of one, two and four segments that wait for their neighbours: every variant
   // joins the eight in this tree, whichever waves took them.
@@ -508,29 +503,37 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
       });
     }
   };
-  int i = 0;
-  for (; i < steps; i += kRing) {
-    if ((i & (chunk - 1)) == 0) {
-      if (i) __syncthreads();
-      if constexpr (kSplit == 0) fetch_step(i);
-      if ((i & ((1 << plan.log_scales) - 1)) == 0) {
-        if (pairs) stage_scales(i, Bool<true>{});
-        else stage_scales(i, Bool<false>{});
-      }
-      put_step(i);
-      __syncthreads();
-      if constexpr (kSums) {
-        stage_sums();
-        __syncthreads();
-      }
-      if constexpr (kSplit != 0) fetch_step(i + 1);
-      __builtin_amdgcn_sched_barrier(0);
+  auto stage = [&](int i) {
+    if ((i & (chunk - 1)) != 0) return;
+    if (i) __syncthreads();
+    if constexpr (kSplit == 0) fetch_step(i);
+    if ((i & ((1 << plan.log_scales) - 1)) == 0) {
+      if (pairs) stage_scales(i, Bool<true>{});
+      else stage_scales(i, Bool<false>{});
     }
-    if (kRing == 2 && i + 1 == steps) break;
+    put_step(i);
+    __syncthreads();
+    if constexpr (kSums) {
+      stage_sums();
+      __syncthreads();
+    }
+    if constexpr (kSplit != 0) fetch_step(i + 1);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // two steps a round, so that each knows its place in the ring; the last of an odd number follows
+  const int rounds = steps & ~(kRing - 1);
+  int i = 0;
+  for (; i < rounds; i += kRing) {
+    stage(i);
     step(i, ring[0]);
-    if constexpr (kRing == 2) step(i + 1, ring[1]);
+    if constexpr (kRing == 2) step(i + 1, ring[1]);     // (a chunk has two steps or more)
   }
-  if (i < steps) step(i, ring[0]);
+  if constexpr (kRing == 2) {
+    if (i < steps) {
+      stage(i);
+      step(i, ring[0]);
+    }
+  }
   close_segments(units);
 
   auto store = [&](int t, int mt, int j, float v) {
@@ -611,7 +614,7 @@ hipError_t linear_tiles(const LinearParams& p, hipStream_t stream) {
   const int tiles = (p.N + 15) / 16;
   if constexpr (TK <= 4) {
     // as many waves along K as give the card 2048 waves or more: 14336 rows of
-    // 7168 take 15.4 us with four, 17.1 with two, 21 with eight
+    // 7168 take 15 us with four, 17 with two, 21 with eight
     const int units = (p.K + 255) / 256;
     int split = 1;
     while (split < 8 && split * 2 <= units && split * tiles < 2048) split *= 2;
