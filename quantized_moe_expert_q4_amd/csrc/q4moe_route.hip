@@ -417,20 +417,24 @@ __global__ __launch_bounds__(kWaves * 64) void route_backward_kernel(RouteBackwa
     const __amdgpu_buffer_rsrc_t dst =
         make_rsrc(static_cast<uint8_t*>(p.d_logits) + (size_t)t0 * pitch, (uint32_t)tokens * pitch);
     const uint32_t row = (uint32_t)group * pitch;
-    // lane l holds the places l, l + L, ...
+    // lane l holds the places l, l + L, ...; an id that names no expert is
+    // dropped here: it could name a padding expert, whose score of 0 would
+    // still carry an infinite or NaN gradient into the row's sums
+    const auto named = [&](int e) { return (uint32_t)e < (uint32_t)p.E ? e : -1; };
     const size_t places = (size_t)t * p.K;
     int id = in && l < p.K ? p.ids[places + l] : -1;
     float dw = in && l < p.K && p.d_weights ? p.d_weights[places + l] : 0.0f;
     float x[VPT], s[VPT], sum;
     load_row<L, VPT>(src, p.lf32, row, p.E, l, x);
     const bool here = __shfl(id, 0, L) >= 0;
+    id = named(id);
     scores<L, VPT, float>(x, p.sigmoid, s, sum);
     // g: the gradients that reach each expert, n: the places that chose it
     float g[VPT] = {};
     int n[VPT] = {};
     for (int j = 0; j < p.K; ++j) {
       if (j && j % L == 0) {
-        id = in && j + l < p.K ? p.ids[places + j + l] : -1;
+        id = in && j + l < p.K ? named(p.ids[places + j + l]) : -1;
         dw = in && j + l < p.K && p.d_weights ? p.d_weights[places + j + l] : 0.0f;
       }
       const int e = __shfl(id, j % L, L) - l;
