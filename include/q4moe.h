@@ -573,7 +573,9 @@ enum { Q4_SCORE_SOFTMAX = 0, Q4_SCORE_SIGMOID = 1 };
  *   counts[e]    = number of (token, place) pairs that chose e          (int32)
  *   loss         = E * sum_e (counts[e] / (K T)) * (1/T) sum_t p[t,e]   (F32)
  *   loss_grad[e] = d loss / d p[t,e] = E * counts[e] / (K T^2)          (F32)
- * p[t] is the score over its sum (softmax: the score).  T = 0 gives zeros.
+ * p[t] is the score over its sum (softmax: the score).  T = 0 gives zeros.  The
+ * p[t,e] are F32; their sums over the tokens add at most 64 roundings of F32
+ * (2^-24 relative each) whatever M.
  *   select_bias  device F32 [E] or NULL; token_mask device uint8 [M] or NULL.
  *   ids          device int32 [M][K]; weights device F32 [M][K].
  *   workspace    device, 256-byte aligned, q4_route_workspace_bytes(M, E)

@@ -28,6 +28,7 @@ constexpr int kWaves = 8;            // waves of a work-group
 constexpr int kMaxBlocks = 256;      // work-groups of a call with statistics
 constexpr int kStatThreads = 256;
 constexpr int kStatExperts = 32;     // experts of a work-group that joins the statistics
+constexpr int kRun = 32;             // tokens whose probabilities a lane adds up in F32
 
 // Lane l's logits of the row at byte offset `row` (-inf where there is no
 // expert).  The type is asked once, so that the loads are in flight together.
@@ -245,13 +246,16 @@ struct Partials {
   }
 };
 
-template <int L, int VPT>
+// STATS: with the batch statistics (p.partials).  They have kernels of their own
+// for the registers of their sums: with them 257..512 experts take 141, which
+// would leave the call without statistics one work-group a CU instead of two.
+template <int L, int VPT, bool STATS>
 __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
   constexpr int G = 64 / L;          // tokens of a wave
   constexpr int kRow = L * VPT + 16; // floats of a token's scores in LDS (the four tokens on different banks)
   __shared__ float s_score[kWaves][G][kRow];
   __shared__ int s_pick[kWaves][G][kRouteMaxTopK];
-  __shared__ int s_count[L * VPT];
+  __shared__ int s_count[STATS ? L * VPT : 1];
   __shared__ int s_tokens;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -259,9 +263,12 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
   int* const pick = s_pick[wave][group];
   float* const score = s_score[wave][group];
   const uint32_t pitch = (uint32_t)p.E * (p.lf32 ? 4u : 2u);
+  // a lane's sums over its tokens: kRun of them in F32, the runs in double
   float psum[VPT] = {}, bias[VPT];
+  double psums[VPT] = {};
+  int in_run = 0;
   load_experts<L, VPT>(p.bias, p.E, l, bias);
-  if (p.partials) {
+  if constexpr (STATS) {
     for (int e = threadIdx.x; e < L * VPT; e += kWaves * 64) s_count[e] = 0;
     if (threadIdx.x == 0) s_tokens = 0;
     __syncthreads();
@@ -303,23 +310,32 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
         if (e >= 0) {
           w = score[e];
           if (p.renormalize) w = total == 0.0f ? 0.0f : w / total;
-          if (p.partials) atomicAdd(&s_count[e], 1);
+          if constexpr (STATS) atomicAdd(&s_count[e], 1);
         }
         p.ids[(size_t)t * p.K + j] = e;
         p.weights[(size_t)t * p.K + j] = w * p.scale;
       }
     }
-    if (p.partials) {
+    if constexpr (STATS) {
       if (l == 0 && here) atomicAdd(&s_tokens, 1);
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) psum[v] += here ? s[v] * inv : 0.0f;
+      if (++in_run == kRun) {
+        in_run = 0;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          psums[v] += (double)psum[v];
+          psum[v] = 0.0f;
+        }
+      }
     }
     wave_sync();
   }
-  if (!p.partials) return;
+  if constexpr (!STATS) return;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
+    psum[v] = (float)(psums[v] + (double)psum[v]);
     if constexpr (G > 1) {             // the wave's four tokens, in one order
       const auto add = [](float a, float b) { return a + b; };
       psum[v] = join_rows<false>(psum[v], add);
@@ -517,12 +533,12 @@ hipError_t run(const void* const (&kernels)[10], const P& p, int blocks, hipStre
   return hipLaunchKernel(kernels[i], dim3((unsigned)blocks), dim3(kWaves * 64), args, 0, stream);
 }
 
-#define Q4_ROUTE_KERNELS(k)                                                                             \
-  {reinterpret_cast<const void*>(&k<16, 1>), reinterpret_cast<const void*>(&k<16, 2>),                  \
-   reinterpret_cast<const void*>(&k<16, 4>), reinterpret_cast<const void*>(&k<16, 8>),                  \
-   reinterpret_cast<const void*>(&k<16, 16>), reinterpret_cast<const void*>(&k<64, 1>),                 \
-   reinterpret_cast<const void*>(&k<64, 2>), reinterpret_cast<const void*>(&k<64, 4>),                  \
-   reinterpret_cast<const void*>(&k<64, 8>), reinterpret_cast<const void*>(&k<64, 16>)}
+// A kernel's variants by lanes of a token and experts of a lane.
+#define Q4_ROUTE_KERNELS(k) \
+  {k(16, 1), k(16, 2), k(16, 4), k(16, 8), k(16, 16), k(64, 1), k(64, 2), k(64, 4), k(64, 8), k(64, 16)}
+#define Q4_ROUTE_PLAIN(L, VPT) reinterpret_cast<const void*>(&route_kernel<L, VPT, false>)
+#define Q4_ROUTE_STATS(L, VPT) reinterpret_cast<const void*>(&route_kernel<L, VPT, true>)
+#define Q4_ROUTE_BACKWARD(L, VPT) reinterpret_cast<const void*>(&route_backward_kernel<L, VPT>)
 
 }  // namespace
 
@@ -532,11 +548,13 @@ size_t route_partial_bytes(int64_t M, int64_t E) {
 }
 
 hipError_t launch_route(const RouteParams& p, hipStream_t stream) {
-  static const void* const kernels[10] = Q4_ROUTE_KERNELS(route_kernel);
+  static const void* const plain[10] = Q4_ROUTE_KERNELS(Q4_ROUTE_PLAIN);
+  static const void* const stats[10] = Q4_ROUTE_KERNELS(Q4_ROUTE_STATS);
   const int all = token_blocks(p.M, p.E);
-  const int blocks = p.partials ? stat_blocks(p.M, p.E) : (all < 65536 ? all : 65536);
-  hipError_t e = run(kernels, p, blocks, stream);
-  if (e != hipSuccess || !p.partials) return e;
+  if (!p.partials) return run(plain, p, all < 65536 ? all : 65536, stream);
+  const int blocks = stat_blocks(p.M, p.E);
+  const hipError_t e = run(stats, p, blocks, stream);
+  if (e != hipSuccess) return e;
   RouteParams q = p;
   int nb = blocks;
   void* args[] = {&q, &nb};
@@ -545,7 +563,7 @@ hipError_t launch_route(const RouteParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_route_backward(const RouteBackwardParams& p, hipStream_t stream) {
-  static const void* const kernels[10] = Q4_ROUTE_KERNELS(route_backward_kernel);
+  static const void* const kernels[10] = Q4_ROUTE_KERNELS(Q4_ROUTE_BACKWARD);
   const int all = token_blocks(p.M, p.E);
   return run(kernels, p, all < 65536 ? all : 65536, stream);
 }
