@@ -579,7 +579,9 @@ enum { Q4_SCORE_SOFTMAX = 0, Q4_SCORE_SIGMOID = 1 };
  *   select_bias  device F32 [E] or NULL; token_mask device uint8 [M] or NULL.
  *   ids          device int32 [M][K]; weights device F32 [M][K].
  *   workspace    device, 256-byte aligned, q4_route_workspace_bytes(M, E)
- *                bytes; may be NULL when counts, loss and loss_grad are.
+ *                bytes; may be NULL when counts, loss and loss_grad are.  The
+ *                size falls with neither M nor E: a workspace for the largest
+ *                batch serves every smaller one.
  * Limits: 1 <= M <= 2^24, 1 <= E <= 1024, 1 <= K <= min(E, 64).
  */
 size_t q4_route_workspace_bytes(int64_t M, int64_t E);

@@ -542,8 +542,11 @@ hipError_t run(const void* const (&kernels)[10], const P& p, int blocks, hipStre
 
 }  // namespace
 
+// For as many work-groups as any smaller batch has: those of 64 lanes a token,
+// whatever lanes this one takes.
 size_t route_partial_bytes(int64_t M, int64_t E) {
-  const size_t bytes = kTokensAt + (size_t)stat_blocks((int)M, (int)E) * (2 * (size_t)E + 1) * 4;
+  const int64_t most = (M + kWaves - 1) / kWaves;
+  const size_t bytes = kTokensAt + (size_t)(most < kMaxBlocks ? most : kMaxBlocks) * (2 * (size_t)E + 1) * 4;
   return (bytes + 255) / 256 * 256;
 }
 
