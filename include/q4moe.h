@@ -611,13 +611,21 @@ int q4_route_backward_f32(const void *logits_f32, int64_t M, int64_t E, int64_t 
                           int renormalize, float scale, const int32_t *ids, const float *d_weights,
                           const float *d_loss, const float *loss_grad, void *d_logits_f32,
                           q4_stream_t stream);
-int q4_validate_route(const void *logits, int64_t M, int64_t E, int64_t K, int score,
+int q4_validate_route(const void *logits_bf16, int64_t M, int64_t E, int64_t K, int score,
                       const float *select_bias, const uint8_t *token_mask, const int32_t *ids,
                       const float *weights, const int32_t *counts, const float *loss,
                       const float *loss_grad, const void *workspace, size_t workspace_bytes);
-int q4_validate_route_backward(const void *logits, int64_t M, int64_t E, int64_t K, int score,
+int q4_validate_route_f32(const void *logits_f32, int64_t M, int64_t E, int64_t K, int score,
+                          const float *select_bias, const uint8_t *token_mask, const int32_t *ids,
+                          const float *weights, const int32_t *counts, const float *loss,
+                          const float *loss_grad, const void *workspace, size_t workspace_bytes);
+int q4_validate_route_backward(const void *logits_bf16, int64_t M, int64_t E, int64_t K, int score,
                                const int32_t *ids, const float *d_weights, const float *d_loss,
-                               const float *loss_grad, const void *d_logits);
+                               const float *loss_grad, const void *d_logits_bf16);
+int q4_validate_route_backward_f32(const void *logits_f32, int64_t M, int64_t E, int64_t K,
+                                   int score, const int32_t *ids, const float *d_weights,
+                                   const float *d_loss, const float *loss_grad,
+                                   const void *d_logits_f32);
 
 /*
  * Combination of the expert outputs q4_expert_forward_grouped writes:

@@ -161,11 +161,11 @@ for _suffix in ("", "_f32"):
     _SIGNATURES["q4_route" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P, _P, _P,
                                                 _SZ, _P])
     _SIGNATURES["q4_route_backward" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P])
+    _SIGNATURES["q4_validate_route" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _SZ])
+    _SIGNATURES["q4_validate_route_backward" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P])
     _SIGNATURES["q4_combine" + _suffix] = (_INT, [_P, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P])
     _SIGNATURES["q4_combine_backward" + _suffix] = (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P])
 _SIGNATURES["q4_route_workspace_bytes"] = (_SZ, [_I64, _I64])
-_SIGNATURES["q4_validate_route"] = (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _SZ])
-_SIGNATURES["q4_validate_route_backward"] = (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P])
 _SIGNATURES["q4_validate_combine"] = (_INT, [_P, _P, _P, _I64, _P, _I64, _I64, _I64, _P])
 _SIGNATURES["q4_validate_combine_backward"] = (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P])
 
@@ -534,11 +534,11 @@ def route(logits, M: int, E: int, K: int, ids, weights, score: str = "softmax", 
 
 def validate_route(logits, M: int, E: int, K: int, ids, weights, score: str = "softmax", select_bias=None,
                    token_mask=None, counts=None, loss=None, loss_grad=None, workspace=None,
-                   workspace_bytes: int = 0) -> int:
+                   workspace_bytes: int = 0, xdtype: str = "bf16") -> int:
     """Host-only argument check of the router; returns the status."""
-    return load().q4_validate_route(_ptr(logits), M, E, K, _score(score), _ptr(select_bias), _ptr(token_mask), _ptr(ids),
-                                    _ptr(weights), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(workspace),
-                                    workspace_bytes)
+    return _fn(load(), "q4", "validate_route", xdtype)(
+        _ptr(logits), M, E, K, _score(score), _ptr(select_bias), _ptr(token_mask), _ptr(ids), _ptr(weights), _ptr(counts),
+        _ptr(loss), _ptr(loss_grad), _ptr(workspace), workspace_bytes)
 
 
 def route_backward(logits, M: int, E: int, K: int, ids, d_logits, d_weights=None, d_loss=None, loss_grad=None,
@@ -554,10 +554,10 @@ def route_backward(logits, M: int, E: int, K: int, ids, d_logits, d_weights=None
 
 
 def validate_route_backward(logits, M: int, E: int, K: int, ids, d_logits, d_weights=None, d_loss=None,
-                            loss_grad=None, score: str = "softmax") -> int:
+                            loss_grad=None, score: str = "softmax", xdtype: str = "bf16") -> int:
     """Host-only argument check of the router's gradient; returns the status."""
-    return load().q4_validate_route_backward(_ptr(logits), M, E, K, _score(score), _ptr(ids), _ptr(d_weights),
-                                             _ptr(d_loss), _ptr(loss_grad), _ptr(d_logits))
+    return _fn(load(), "q4", "validate_route_backward", xdtype)(
+        _ptr(logits), M, E, K, _score(score), _ptr(ids), _ptr(d_weights), _ptr(d_loss), _ptr(loss_grad), _ptr(d_logits))
 
 
 def combine(y, weights, M: int, K: int, H: int, out, slot_ids=None, num_slots: int = 0, base=None, stream=None,

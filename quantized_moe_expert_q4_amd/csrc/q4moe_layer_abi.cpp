@@ -79,7 +79,7 @@ int check_route_sizes(int64_t M, int64_t E, int64_t K, int score) {
   return Q4_OK;
 }
 
-// `logit_align` is the size of a logit; the type-blind validators pass 2.
+// `logit_align` is the size of a logit.
 int check_route(uintptr_t logit_align, const void* logits, int64_t M, int64_t E, int64_t K, int score,
                 const float* bias, const uint8_t* mask, const int32_t* ids, const float* weights,
                 const int32_t* counts, const float* loss, const float* loss_grad, const void* ws, size_t ws_bytes) {
@@ -299,17 +299,30 @@ int q4_route_backward_f32(const void* logits_f32, int64_t M, int64_t E, int64_t 
                             d_logits_f32, stream);
 }
 
-int q4_validate_route(const void* logits, int64_t M, int64_t E, int64_t K, int score, const float* select_bias,
+int q4_validate_route(const void* logits_bf16, int64_t M, int64_t E, int64_t K, int score, const float* select_bias,
                       const uint8_t* token_mask, const int32_t* ids, const float* weights, const int32_t* counts,
                       const float* loss, const float* loss_grad, const void* workspace, size_t workspace_bytes) {
-  return check_route(2, logits, M, E, K, score, select_bias, token_mask, ids, weights, counts, loss, loss_grad,
+  return check_route(2, logits_bf16, M, E, K, score, select_bias, token_mask, ids, weights, counts, loss, loss_grad,
                      workspace, workspace_bytes);
 }
 
-int q4_validate_route_backward(const void* logits, int64_t M, int64_t E, int64_t K, int score, const int32_t* ids,
+int q4_validate_route_f32(const void* logits_f32, int64_t M, int64_t E, int64_t K, int score, const float* select_bias,
+                          const uint8_t* token_mask, const int32_t* ids, const float* weights, const int32_t* counts,
+                          const float* loss, const float* loss_grad, const void* workspace, size_t workspace_bytes) {
+  return check_route(4, logits_f32, M, E, K, score, select_bias, token_mask, ids, weights, counts, loss, loss_grad,
+                     workspace, workspace_bytes);
+}
+
+int q4_validate_route_backward(const void* logits_bf16, int64_t M, int64_t E, int64_t K, int score, const int32_t* ids,
                                const float* d_weights, const float* d_loss, const float* loss_grad,
-                               const void* d_logits) {
-  return check_route_backward(2, logits, M, E, K, score, ids, d_weights, d_loss, loss_grad, d_logits);
+                               const void* d_logits_bf16) {
+  return check_route_backward(2, logits_bf16, M, E, K, score, ids, d_weights, d_loss, loss_grad, d_logits_bf16);
+}
+
+int q4_validate_route_backward_f32(const void* logits_f32, int64_t M, int64_t E, int64_t K, int score,
+                                   const int32_t* ids, const float* d_weights, const float* d_loss,
+                                   const float* loss_grad, const void* d_logits_f32) {
+  return check_route_backward(4, logits_f32, M, E, K, score, ids, d_weights, d_loss, loss_grad, d_logits_f32);
 }
 
 int q4_combine(const void* y_bf16, const float* weights, const int32_t* slot_ids, int64_t num_slots,
