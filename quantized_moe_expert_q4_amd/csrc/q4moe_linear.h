@@ -164,11 +164,12 @@ struct Bool {
   static constexpr bool value = V;
 };
 
-// What a launch chose: S waves along K (1, 2, 4 or 8), the steps of S units
-// (powers of two) whose tokens and whose scales are staged in LDS together, and
-// the bytes there of the tokens, of their sums, of a row's scales and of all
-// rows' scales.
+// What a launch chose: its first work-group along the rows, S waves along K (1,
+// 2, 4 or 8), the steps of S units (powers of two) whose tokens and whose scales
+// are staged in LDS together, and the bytes there of the tokens, of their sums,
+// of a row's scales and of all rows' scales.
 struct LinearPlan {
+  int block0;
   int S, shift, log_chunk, log_scales;
   int x_bytes, xs_bytes, pitch, scale_bytes;
 };
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
   const int S = kSplit ? kSplit : plan.S, shift = kSplit ? __builtin_ctz(kSplit) : plan.shift;
   const int log_chunk = kSplit ? 0 : plan.log_chunk, chunk = 1 << log_chunk;
   const int ks = wave & (S - 1), set = wave >> shift, sets = kLinearWaves >> shift;
-  const int wg_row0 = (int)blockIdx.x * sets * (16 * T), row0 = wg_row0 + set * (16 * T);
+  const int wg_row0 = (plan.block0 + (int)blockIdx.x) * sets * (16 * T), row0 = wg_row0 + set * (16 * T);
   const int m0 = (int)blockIdx.y * TK;
   const int tokens = min(TK, p.M - m0);
   const int units = (p.K + 255) / 256;
@@ -567,6 +568,10 @@ __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) voi
 constexpr int kLinearStage = 72 * 1024;
 // Most that it takes.
 constexpr int kLinearLds = 144 * 1024;
+// Work-groups along the rows of one launch: a grid takes fewer than 2^32 threads
+// there, which five tokens or more (64 rows a work-group) of the most rows of
+// eight weights reach.
+constexpr int kLinearBlocks = 1 << 22;
 
 template <int KPG, bool AFF, bool SF, bool XF, int TK, int T, int kSplit>
 hipError_t linear_launch(const LinearParams& p, int split, hipStream_t stream) {
@@ -603,8 +608,14 @@ hipError_t linear_launch(const LinearParams& p, int split, hipStream_t stream) {
   LinearParams q = p;
   void* args[] = {&q, &plan};
   const void* const f = reinterpret_cast<const void*>(&linear_kernel<KPG, AFF, SF, XF, TK, T, kSplit>);
-  return hipLaunchKernel(f, dim3((unsigned)((p.N + 16 * T * sets - 1) / (16 * T * sets)), (unsigned)((p.M + TK - 1) / TK)),
-                         dim3(kLinearWaves * 64), args, lds, stream);
+  const int blocks = (p.N + 16 * T * sets - 1) / (16 * T * sets);
+  for (; plan.block0 < blocks; plan.block0 += kLinearBlocks) {
+    const int here = blocks - plan.block0 < kLinearBlocks ? blocks - plan.block0 : kLinearBlocks;
+    const hipError_t e = hipLaunchKernel(f, dim3((unsigned)here, (unsigned)((p.M + TK - 1) / TK)), dim3(kLinearWaves * 64),
+                                         args, lds, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Row tiles of a wave and waves along K (figures: one call, bf16 tokens
