@@ -47,10 +47,12 @@ class MoeLayer:
         self.expert_ws = aligned_empty(self.expert_bytes, 256)
         self.route_bytes = q4.route_workspace_bytes(M, E)
         self.route_ws = aligned_empty(self.route_bytes, 256)
+        self.tokens, self.stats = 0, False      # of the last forward
 
     def forward(self, x, residual=None, token_mask=None, stats=False):
         """The layer's output for the bf16 rows ``x``; with ``stats`` also ``counts``, ``loss`` and ``loss_grad``."""
         M = x.shape[0]
+        self.tokens, self.stats = 0, False
         weights, scales, biases = self.gate
         q4.linear(weights, scales, x, M, self.E, self.H, self.group, self.logits, biases=biases)
         stat = dict(counts=self.counts, loss=self.loss, loss_grad=self.loss_grad, workspace=self.route_ws,
@@ -61,16 +63,22 @@ class MoeLayer:
                                   self.I, self.mid, self.y, self.expert_ws, self.expert_bytes)
         q4.combine(self.y, self.weights, M, self.K, self.H, self.out, slot_ids=self.ids, num_slots=self.E,
                    base=residual)
+        self.tokens, self.stats = M, stats
         return self.out[:M]
 
-    def backward(self, d_out, d_loss):
-        """Gradients of the router's logits (through the weights and ``d_loss`` times
-        the balance loss) and of the expert outputs, of the last forward with ``stats``."""
+    def backward(self, d_out, d_loss=None):
+        """Gradients of the router's logits (through the weights and, with ``d_loss``, ``d_loss``
+        times the balance loss) and of the expert outputs, of the last forward; ``d_loss``
+        needs its ``stats``."""
         M = d_out.shape[0]
+        if M != self.tokens:
+            raise ValueError(f"the last forward had {self.tokens} tokens, not {M}")
+        if d_loss is not None and not self.stats:
+            raise ValueError("the gradient of the balance loss needs a forward with stats")
         q4.combine_backward(d_out, self.y, self.weights, M, self.K, self.H, d_y=self.d_y, d_weights=self.d_weights,
                             slot_ids=self.ids, num_slots=self.E)
         q4.route_backward(self.logits, M, self.E, self.K, self.ids, self.d_logits, d_weights=self.d_weights,
-                          d_loss=d_loss, loss_grad=self.loss_grad, **self.kw)
+                          d_loss=d_loss, loss_grad=None if d_loss is None else self.loss_grad, **self.kw)
         return self.d_logits[:M], self.d_y[:M]
 
 
