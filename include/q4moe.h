@@ -530,6 +530,9 @@ enum { Q4_SCALE_BF16 = 0, Q4_SCALE_F32 = 1 };
  * result of a token does not depend on the other tokens of the call or their
  * number.  A token that holds an infinity or a NaN, or whose 31 * |x| leave the
  * F32 range when summed over a group, has results that are not finite.
+ * x_f32 enters as three bf16 parts of eight bits, the smallest of which is
+ * 2^-133: values below 2^-110 are taken to a multiple of that, towards zero,
+ * larger ones whole.
  *   weights  device, K/2 bytes a row, N rows, 16-byte aligned.
  *   scales, biases  device, [N][ceil(K/group)], bf16 or F32 by scale_type,
  *            aligned to their type; the last group of a row may be short.
