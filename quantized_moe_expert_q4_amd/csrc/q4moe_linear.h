@@ -635,9 +635,13 @@ hipError_t linear_tiles(const LinearParams& p, hipStream_t stream) {
   } else {
     constexpr int S = XF && TK == 32 ? 2 : 4;
     if constexpr (!XF && TK <= 16) {
-      // few rows: all waves along K (16 tokens, 4096 rows of 4096: 8.8 us
-      // against 10.3; 6144 rows: 12.3 us with four against 18.3)
-      if (tiles * 8 < 3000) return linear_launch<KPG, AFF, SF, XF, TK, 1, 8>(p, 0, stream);
+      // few rows: all waves along K, as long as every work-group has a CU of its
+      // own (their tokens and sums take one each).  16 tokens, rows of 7168:
+      // 4096 of them take 11.9 us against 12.6 with four waves, 4112 take 15.8
+      // against 12.8; groups of 32 with biases 15.3 against 18.2 and 27.4
+      // against 18.1.  (Eight tokens of 14336 alone would gain on, 18.3 against 19.5.)
+      constexpr int kCus = 256;
+      if (tiles <= kCus) return linear_launch<KPG, AFF, SF, XF, TK, 1, 8>(p, 0, stream);
     }
     // two tiles of a wave share the tokens' reads from LDS, once there are more
     // work-groups than the 256 CUs hold at a time (one each by their LDS or
