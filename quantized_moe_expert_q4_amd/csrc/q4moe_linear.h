@@ -645,11 +645,26 @@ hipError_t linear_tiles(const LinearParams& p, hipStream_t stream) {
     }
     // two tiles of a wave share the tokens' reads from LDS, once there are more
     // work-groups than the 256 CUs hold at a time (one each by their LDS or
-    // registers, two of the smaller variants): 32 tokens of 4096 take 14.9 us
-    // against 18.3 with 8192 rows (256 work-groups), 23.6 against 16.4 with 10240
-    const int groups = (tiles * S + kLinearWaves - 1) / kLinearWaves * ((p.M + TK - 1) / TK);
-    constexpr int kAtOnce = 256 * (TK * (XF ? 2 : 1) <= 16 ? 2 : 1);
-    if (groups > kAtOnce) return linear_launch<KPG, AFF, SF, XF, TK, 2, S>(p, 0, stream);
+    // registers, two of the smaller variants).  Rows of 4096, one tile against
+    // two: 32 tokens 18.3 us against 14.9 with 8192 rows (256 work-groups), 16.4
+    // against 23.6 with 10240, 44.1 against 30.9 with 32768; 16 tokens 25.4
+    // against 23.7 and 8 tokens 22.7 against 19.6 with 32768 (groups of 64
+    // without biases).  With up to 16 tokens, where four waves a SIMD leave 128
+    // registers, the two tiles spill some of them, most with biases of small
+    // groups: 16 tokens and groups of 32 never gain (24576 rows 24.4 against
+    // 32.3, 131072 rows 112 against 119), groups of 64 from 65536 rows on (20.6
+    // against 24.6 with 24576, 48.3 against 48.4, 96.9 against 89.8 with
+    // 131072).  Eight float tokens have two work-groups a CU with one tile and
+    // one with two: groups of 128 gain from 32768 rows on (24.1 against 26.0
+    // with 24576, 30.7 against 27.0), smaller ones lose up to 35% below and gain
+    // 5% at most at 131072.
+    constexpr bool kFew = TK * (XF ? 2 : 1) <= 16;
+    constexpr bool kTwo = !kFew || (XF ? KPG == 4 : !AFF || KPG > 1);
+    if constexpr (kTwo) {
+      constexpr int kAtOnce = !kFew ? 256 : XF ? 900 : AFF && KPG == 2 ? 2000 : 512;
+      const int groups = (tiles * S + kLinearWaves - 1) / kLinearWaves * ((p.M + TK - 1) / TK);
+      if (groups > kAtOnce) return linear_launch<KPG, AFF, SF, XF, TK, 2, S>(p, 0, stream);
+    }
     return linear_launch<KPG, AFF, SF, XF, TK, 1, S>(p, 0, stream);
   }
 }

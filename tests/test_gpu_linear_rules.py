@@ -25,3 +25,13 @@ def exact_and_alone(M, N, K, group, affine, scales, kind):
 @pytest.mark.parametrize("M,N,K", [(8, 4096, 2056), (8, 4097, 2056), (16, 4089, 1032), (16, 4112, 1032), (11, 5990, 520), (16, 6011, 264)])
 def test_waves_along_the_row(M, N, K, group, affine):
     exact_and_alone(M, N, K, group, affine, "bf16", "bf16")
+
+
+# (M, N): one and two row tiles of a wave for up to 8, 16, 32 and 64 tokens of a work-group
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("affine", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N", [(5, 16384), (5, 16411), (8, 28817), (7, 65555), (9, 8209), (16, 16411), (12, 65555), (29, 8209),
+                                 (40, 4001), (70, 8209)])
+def test_row_tiles(M, N, group, affine, kind):
+    exact_and_alone(M, N, 392, group, affine, "bf16" if group == 64 else "f32", kind)
