@@ -538,6 +538,8 @@ enum { Q4_SCALE_BF16 = 0, Q4_SCALE_F32 = 1 };
  *            aligned to their type; the last group of a row may be short.
  *   group    32, 64 or 128.
  *   x        device, [M][K], 16-byte aligned; out device, [M][N], aligned to its type.
+ * Made for up to 64 tokens: more are taken 64 (float: 32) at a time, and each
+ * such pass reads and unpacks the weights again.
  * Limits: 1 <= M <= 65535, 8 <= K <= 65536 with K % 8 == 0, 1 <= N,
  * N*K/2 <= 2^31 - 16.
  */
@@ -564,6 +566,7 @@ enum { Q4_SCORE_SOFTMAX = 0, Q4_SCORE_SIGMOID = 1 };
  *             when select_bias is given, best first, ties to the lowest index;
  *   w_j     = scale * score_{ids_j}, divided by the sum of the chosen scores
  *             when renormalize != 0 (0 when that sum is 0).
+ * Scores are F32; a sigmoid below 2^-126 counts as 0.
  * An expert whose logit (or bias) is -inf is never chosen: places left over
  * hold id -1 and weight 0, which the grouped calls answer with zero rows and
  * q4_combine skips.  A token whose mask byte is 0, or that can choose no expert,
@@ -653,6 +656,7 @@ int q4_combine_f32(const void *y_f32, const float *weights, const int32_t *slot_
  *   d_weights[t,j] = sum_h d_out[t,h] * y[t,j,h]             (F32)
  * zero for a pair that was left out; base's gradient is d_out.  d_y or
  * d_weights may be NULL (not both); y may be NULL when d_weights is.
+ * d_y is for a caller that has the experts' own gradient: this library has none.
  */
 int q4_combine_backward(const void *d_out_bf16, const void *y_bf16, const float *weights,
                         const int32_t *slot_ids, int64_t num_slots, int64_t M, int64_t K, int64_t H,

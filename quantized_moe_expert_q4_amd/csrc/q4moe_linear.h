@@ -16,10 +16,14 @@
 //
 // What bounds it (one call, bf16 unless said).  One token: the weight stream,
 // 131072 x 4096 with biases in 50 us (5.7 TB/s; its vector instructions alone
-// take about 39); 14336 x 7168 in 15.  Many: 64 tokens of 14336 x 7168 in 41 us,
-// where a step's vector instructions (3600 cycles a SIMD), LDS reads (2800) and
-// matrix operations (1400) overlap little at two waves a SIMD; 16 tokens 19 us,
-// 64 float tokens 65.  Few rows: steps of about 3 us each, bound by latency.
+// take about 39); 14336 x 7168 in 15.  One float token through the former in 80
+// us: its exact unpacking takes the vector units more than twice the work.
+// Many: 64 tokens of 14336 x 7168 in 41 to 43 us, where a step's vector
+// instructions (3600 cycles a SIMD), LDS reads (2800) and matrix operations
+// (1400) overlap little at two waves a SIMD; 16 tokens 19 us, 64 float tokens 65.
+// More are taken 64 (float: 32) at a time and unpack the weights each time: 4096
+// tokens take 2.1 ms, which the matrix operations alone would take 0.6 of.  Few
+// rows: steps of about 3 us each, bound by latency.
 //
 // Unpacking.  Bits 3..6 of a bf16 in [16, 32) count in steps of one: a nibble
 // q moved there under the bit pattern of 16 is the number 16 + q, exactly, two
@@ -179,7 +183,9 @@ struct LinearPlan {
 // row tiles of a wave.  kSplit: waves along K, as the launch chooses (0, up to
 // four tokens) or fixed, so that a step's staged tokens, 64 KB (float: 96 KB) at
 // most, are fetched into a fixed number of registers while the step before is
-// at work.
+// at work.  The four waves a SIMD asked for up to 16 tokens (float: 4) leave 128
+// registers; ten of the two-tile variants spill 12 to 80 bytes a lane over it (the
+// rule in linear_tiles takes them where they gain all the same).
 template <int KPG, bool AFF, bool SF, bool XF, int TK, int T, int kSplit>
 __global__ __launch_bounds__(kLinearWaves * 64, TK <= (XF ? 4 : 16) ? 4 : 2) void linear_kernel(LinearParams p, LinearPlan plan) {
   constexpr int kParts = XF ? 3 : 1;
@@ -671,9 +677,12 @@ hipError_t linear_tiles(const LinearParams& p, hipStream_t stream) {
 
 // Tokens of a work-group: as many as the call has; with too few work-groups
 // fewer, which spreads the tokens over more of them and unpacks the weights for
-// each.  64 tokens of 4096 take 42 us together and 51 in two passes with 14336
-// rows (224 work-groups in one pass), 31 and 15 with 4096 (64), 31, 15 and, in
-// four passes, 11 with 1536 (24).
+// each.  64 tokens of 4096, work-groups with 64, 32 and 16 of them (groups of
+// 128 with biases): 24.6, 30.6 and 28.2 us with 9600 rows (150 work-groups in one
+// pass), 24.6, 16.3 and 19.1 with 8192 (128), 24.2, 13.0 and 19.1 with 4096, 24.3,
+// 12.4 and 10.2 with 1536 (96 work-groups in passes of 32 tokens); rows of 7168
+// and groups of 32 change sides at the same numbers.  32 float tokens, 32 and 16
+// at a time: 30.0 and 19.7 with 8192 rows (128).
 template <int KPG, bool AFF, bool SF, bool XF>
 hipError_t linear_select(const LinearParams& p, hipStream_t stream) {
   constexpr int kEnough = 150;

@@ -15,8 +15,8 @@
 // (with both unrolled in place the router below took 25 us).
 //
 // Measured: 8192 tokens, 256 experts, sigmoid and bias, eight chosen, with the
-// statistics 14.8 + 6.8 us, bound by the instructions of the nine rounds (4 MB
-// of logits are 1 us of memory traffic); its gradient 8.8; one token 3.5.
+// statistics 15 + 6.7 us, bound by the instructions of the nine rounds (4 MB of
+// logits are 1 us of memory traffic); its gradient 8.8; one token 3.4.
 #include "q4moe_device.h"
 #include "q4moe_layer.h"
 
