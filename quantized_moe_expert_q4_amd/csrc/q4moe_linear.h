@@ -652,8 +652,8 @@ hipError_t linear_tiles(const LinearParams& p, hipStream_t stream) {
     // two tiles of a wave share the tokens' reads from LDS, once there are more
     // work-groups than the 256 CUs hold at a time (one each by their LDS or
     // registers, two of the smaller variants).  Rows of 4096, one tile against
-    // two: 32 tokens 18.3 us against 14.9 with 8192 rows (256 work-groups), 16.4
-    // against 23.6 with 10240, 44.1 against 30.9 with 32768; 16 tokens 25.4
+    // two: 32 tokens 14.9 us against 18.3 with 8192 rows (256 work-groups), 23.6
+    // against 16.4 with 10240, 44.1 against 30.9 with 32768; 16 tokens 25.4
     // against 23.7 and 8 tokens 22.7 against 19.6 with 32768 (groups of 64
     // without biases).  With up to 16 tokens, where four waves a SIMD leave 128
     // registers, the two tiles spill some of them, most with biases of small
