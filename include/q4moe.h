@@ -601,6 +601,41 @@ int q4_route_f32(const void *logits_f32, int64_t M, int64_t E, int64_t K, int sc
                  void *workspace, size_t workspace_bytes, q4_stream_t stream);
 
 /*
+ * Router over groups of experts: as q4_route, but a token's experts come from
+ * its top_groups best groups only (group g: experts g * E / groups .. + E /
+ * groups).  A group's rank is the sum over its group_top (1 or 2) best experts
+ * of score_e (+ select_bias_e), in double precision; with group_top 1 and no
+ * select_bias it is the best logit.  Ties go to the lowest index, a NaN ranks
+ * above every number, an expert that cannot be chosen adds nothing, a group
+ * without any that can is never kept.  With top_groups == groups the call is
+ * q4_route.  Gradients: q4_route_backward with the ids of this call.
+ * Limits: those of q4_route; 1 <= groups <= 64 dividing E; 1 <= top_groups <=
+ * groups; K <= top_groups * E / groups.  The workspace is q4_route's.
+ */
+int q4_route_groups(const void *logits_bf16, int64_t M, int64_t E, int64_t K, int64_t groups,
+                    int64_t top_groups, int group_top, int score, int renormalize, float scale,
+                    const float *select_bias, const uint8_t *token_mask, int32_t *ids,
+                    float *weights, int32_t *counts, float *loss, float *loss_grad,
+                    void *workspace, size_t workspace_bytes, q4_stream_t stream);
+int q4_route_groups_f32(const void *logits_f32, int64_t M, int64_t E, int64_t K, int64_t groups,
+                        int64_t top_groups, int group_top, int score, int renormalize, float scale,
+                        const float *select_bias, const uint8_t *token_mask, int32_t *ids,
+                        float *weights, int32_t *counts, float *loss, float *loss_grad,
+                        void *workspace, size_t workspace_bytes, q4_stream_t stream);
+int q4_validate_route_groups(const void *logits_bf16, int64_t M, int64_t E, int64_t K,
+                             int64_t groups, int64_t top_groups, int group_top, int score,
+                             const float *select_bias, const uint8_t *token_mask,
+                             const int32_t *ids, const float *weights, const int32_t *counts,
+                             const float *loss, const float *loss_grad, const void *workspace,
+                             size_t workspace_bytes);
+int q4_validate_route_groups_f32(const void *logits_f32, int64_t M, int64_t E, int64_t K,
+                                 int64_t groups, int64_t top_groups, int group_top, int score,
+                                 const float *select_bias, const uint8_t *token_mask,
+                                 const int32_t *ids, const float *weights, const int32_t *counts,
+                                 const float *loss, const float *loss_grad, const void *workspace,
+                                 size_t workspace_bytes);
+
+/*
  * Gradient of the logits (their type): from d_weights [M][K], the gradient of
  * the weights, and d_loss [1] (device F32), the gradient of the balance loss,
  * whose loss_grad [E] the forward call wrote.  Either may be NULL (d_loss and

@@ -36,12 +36,14 @@ from ._lib import (  # noqa: F401
     stream_read,
     linear,
     route,
+    route_groups,
     route_backward,
     route_workspace_bytes,
     combine,
     combine_backward,
     validate_linear,
     validate_route,
+    validate_route_groups,
     validate_route_backward,
     validate_combine,
     validate_combine_backward,

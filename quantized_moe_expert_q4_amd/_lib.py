@@ -160,6 +160,10 @@ for _suffix in ("", "_f32"):
     _SIGNATURES["q4_validate_linear" + _suffix] = (_INT, [_P, _P, _P, _INT, _I64, _P, _I64, _I64, _I64, _P])
     _SIGNATURES["q4_route" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P, _P, _P,
                                                 _SZ, _P])
+    _SIGNATURES["q4_route_groups" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _INT, _F32, _P, _P,
+                                                       _P, _P, _P, _P, _P, _P, _SZ, _P])
+    _SIGNATURES["q4_validate_route_groups" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _P, _P, _P,
+                                                                _P, _P, _P, _P, _P, _SZ])
     _SIGNATURES["q4_route_backward" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P])
     _SIGNATURES["q4_validate_route" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _SZ])
     _SIGNATURES["q4_validate_route_backward" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P])
@@ -539,6 +543,34 @@ def validate_route(logits, M: int, E: int, K: int, ids, weights, score: str = "s
     return _fn(load(), "q4", "validate_route", xdtype)(
         _ptr(logits), M, E, K, _score(score), _ptr(select_bias), _ptr(token_mask), _ptr(ids), _ptr(weights), _ptr(counts),
         _ptr(loss), _ptr(loss_grad), _ptr(workspace), workspace_bytes)
+
+
+def route_groups(logits, M: int, E: int, K: int, groups: int, top_groups: int, ids, weights, group_top: int = 2,
+                 score: str = "softmax", renormalize: bool = False, scale: float = 1.0, select_bias=None,
+                 token_mask=None, counts=None, loss=None, loss_grad=None, workspace=None, workspace_bytes: int = 0,
+                 stream=None, xdtype: str = "bf16") -> None:
+    """Enqueue the router over groups of experts (see q4_route_groups in
+    include/q4moe.h): as :func:`route`, with every token's experts from its
+    ``top_groups`` best of ``groups`` groups, ranked by the sum of their
+    ``group_top`` best experts."""
+    fn = _fn(load(), "q4", "route_groups", xdtype)
+    _args(("logits", logits, _XDTYPE_NAMES[xdtype], M * E), ("ids", ids, "int32", M * K),
+          ("weights", weights, "float32", M * K), ("select_bias", select_bias, "float32", E),
+          ("token_mask", token_mask, "uint8", M), ("counts", counts, "int32", E), ("loss", loss, "float32", 1),
+          ("loss_grad", loss_grad, "float32", E), ("workspace", workspace, "uint8", workspace_bytes))
+    _check(fn(_ptr(logits), M, E, K, groups, top_groups, group_top, _score(score), int(renormalize), scale,
+              _ptr(select_bias), _ptr(token_mask), _ptr(ids), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(loss_grad),
+              _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def validate_route_groups(logits, M: int, E: int, K: int, groups: int, top_groups: int, ids, weights,
+                          group_top: int = 2, score: str = "softmax", select_bias=None, token_mask=None, counts=None,
+                          loss=None, loss_grad=None, workspace=None, workspace_bytes: int = 0,
+                          xdtype: str = "bf16") -> int:
+    """Host-only argument check of the router over groups; returns the status."""
+    return _fn(load(), "q4", "validate_route_groups", xdtype)(
+        _ptr(logits), M, E, K, groups, top_groups, group_top, _score(score), _ptr(select_bias), _ptr(token_mask),
+        _ptr(ids), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(workspace), workspace_bytes)
 
 
 def route_backward(logits, M: int, E: int, K: int, ids, d_logits, d_weights=None, d_loss=None, loss_grad=None,

@@ -35,6 +35,8 @@ struct RouteParams {
   float scale;
   int M, E, K;
   int sigmoid, renormalize, lf32;
+  int groups, top_groups;     // groups of E / groups experts, of which a token keeps top_groups (0: no groups)
+  int group_top;              // best experts of a group whose keys rank it (1 or 2)
 };
 
 struct RouteBackwardParams {
@@ -66,6 +68,7 @@ hipError_t launch_linear(const LinearParams& p, hipStream_t stream);
 
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopK = 64;
+constexpr int kRouteMaxGroups = 64;
 
 // Bytes of the statistics' workspace for M tokens and E experts.
 size_t route_partial_bytes(int64_t M, int64_t E);

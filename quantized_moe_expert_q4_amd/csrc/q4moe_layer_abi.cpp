@@ -101,13 +101,50 @@ int check_route(uintptr_t logit_align, const void* logits, int64_t M, int64_t E,
   return report(Q4_OK, "");
 }
 
-int run_route(bool f32, const void* logits, int64_t M, int64_t E, int64_t K, int score, int renormalize, float scale,
-              const float* bias, const uint8_t* mask, int32_t* ids, float* weights, int32_t* counts, float* loss,
-              float* loss_grad, void* ws, size_t ws_bytes, q4_stream_t stream) {
-  const int rc = check_route(f32 ? 4 : 2, logits, M, E, K, score, bias, mask, ids, weights, counts, loss, loss_grad,
-                             ws, ws_bytes);
+// Groups of experts (all 0: a router without groups).
+struct Groups {
+  int64_t groups, top_groups;
+  int group_top;
+};
+
+int check_groups(const Groups& g, int64_t E, int64_t K) {
+  if (g.groups < 1 || E < 1 || E % g.groups != 0)
+    return report(Q4_ERR_INVALID_ARGUMENT, "groups must be a positive integer that divides the number of experts");
+  if (g.top_groups < 1 || g.top_groups > g.groups)
+    return report(Q4_ERR_INVALID_ARGUMENT, "top groups must lie between 1 and the number of groups");
+  if (g.group_top != 1 && g.group_top != 2)
+    return report(Q4_ERR_INVALID_ARGUMENT, "a group is ranked by its best 1 or 2 experts");
+  if (g.groups > q4::kRouteMaxGroups) return report(Q4_ERR_UNSUPPORTED, "more than 64 groups is not supported");
+  if (K > g.top_groups * (E / g.groups))
+    return report(Q4_ERR_INVALID_ARGUMENT, "top-k must not exceed the experts of the top groups");
+  return Q4_OK;
+}
+
+int check_route_groups(uintptr_t logit_align, const void* logits, int64_t M, int64_t E, int64_t K, const Groups& g,
+                       int score, const float* bias, const uint8_t* mask, const int32_t* ids, const float* weights,
+                       const int32_t* counts, const float* loss, const float* loss_grad, const void* ws,
+                       size_t ws_bytes) {
+  const int rc = check_route(logit_align, logits, M, E, K, score, bias, mask, ids, weights, counts, loss, loss_grad, ws,
+                             ws_bytes);
+  return rc ? rc : check_groups(g, E, K);
+}
+
+int run_route(bool f32, const void* logits, int64_t M, int64_t E, int64_t K, const Groups* g, int score,
+              int renormalize, float scale, const float* bias, const uint8_t* mask, int32_t* ids, float* weights,
+              int32_t* counts, float* loss, float* loss_grad, void* ws, size_t ws_bytes, q4_stream_t stream) {
+  const uintptr_t size = f32 ? 4 : 2;
+  const int rc = g ? check_route_groups(size, logits, M, E, K, *g, score, bias, mask, ids, weights, counts, loss,
+                                        loss_grad, ws, ws_bytes)
+                   : check_route(size, logits, M, E, K, score, bias, mask, ids, weights, counts, loss, loss_grad, ws,
+                                 ws_bytes);
   if (rc) return rc;
   q4::RouteParams p{};
+  // a token that keeps every group chooses as without groups
+  if (g && g->top_groups < g->groups) {
+    p.groups = (int)g->groups;
+    p.top_groups = (int)g->top_groups;
+    p.group_top = g->group_top;
+  }
   p.logits = logits;
   p.bias = bias;
   p.mask = mask;
@@ -274,15 +311,51 @@ size_t q4_route_workspace_bytes(int64_t M, int64_t E) {
 int q4_route(const void* logits_bf16, int64_t M, int64_t E, int64_t K, int score, int renormalize, float scale,
              const float* select_bias, const uint8_t* token_mask, int32_t* ids, float* weights, int32_t* counts,
              float* loss, float* loss_grad, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
-  return run_route(false, logits_bf16, M, E, K, score, renormalize, scale, select_bias, token_mask, ids, weights,
-                   counts, loss, loss_grad, workspace, workspace_bytes, stream);
+  return run_route(false, logits_bf16, M, E, K, nullptr, score, renormalize, scale, select_bias, token_mask, ids,
+                   weights, counts, loss, loss_grad, workspace, workspace_bytes, stream);
 }
 
 int q4_route_f32(const void* logits_f32, int64_t M, int64_t E, int64_t K, int score, int renormalize, float scale,
                  const float* select_bias, const uint8_t* token_mask, int32_t* ids, float* weights, int32_t* counts,
                  float* loss, float* loss_grad, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
-  return run_route(true, logits_f32, M, E, K, score, renormalize, scale, select_bias, token_mask, ids, weights, counts,
-                   loss, loss_grad, workspace, workspace_bytes, stream);
+  return run_route(true, logits_f32, M, E, K, nullptr, score, renormalize, scale, select_bias, token_mask, ids, weights,
+                   counts, loss, loss_grad, workspace, workspace_bytes, stream);
+}
+
+int q4_route_groups(const void* logits_bf16, int64_t M, int64_t E, int64_t K, int64_t groups, int64_t top_groups,
+                    int group_top, int score, int renormalize, float scale, const float* select_bias,
+                    const uint8_t* token_mask, int32_t* ids, float* weights, int32_t* counts, float* loss,
+                    float* loss_grad, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
+  const Groups g{groups, top_groups, group_top};
+  return run_route(false, logits_bf16, M, E, K, &g, score, renormalize, scale, select_bias, token_mask, ids, weights,
+                   counts, loss, loss_grad, workspace, workspace_bytes, stream);
+}
+
+int q4_route_groups_f32(const void* logits_f32, int64_t M, int64_t E, int64_t K, int64_t groups, int64_t top_groups,
+                        int group_top, int score, int renormalize, float scale, const float* select_bias,
+                        const uint8_t* token_mask, int32_t* ids, float* weights, int32_t* counts, float* loss,
+                        float* loss_grad, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
+  const Groups g{groups, top_groups, group_top};
+  return run_route(true, logits_f32, M, E, K, &g, score, renormalize, scale, select_bias, token_mask, ids, weights,
+                   counts, loss, loss_grad, workspace, workspace_bytes, stream);
+}
+
+int q4_validate_route_groups(const void* logits_bf16, int64_t M, int64_t E, int64_t K, int64_t groups,
+                             int64_t top_groups, int group_top, int score, const float* select_bias,
+                             const uint8_t* token_mask, const int32_t* ids, const float* weights,
+                             const int32_t* counts, const float* loss, const float* loss_grad, const void* workspace,
+                             size_t workspace_bytes) {
+  return check_route_groups(2, logits_bf16, M, E, K, {groups, top_groups, group_top}, score, select_bias, token_mask,
+                            ids, weights, counts, loss, loss_grad, workspace, workspace_bytes);
+}
+
+int q4_validate_route_groups_f32(const void* logits_f32, int64_t M, int64_t E, int64_t K, int64_t groups,
+                                 int64_t top_groups, int group_top, int score, const float* select_bias,
+                                 const uint8_t* token_mask, const int32_t* ids, const float* weights,
+                                 const int32_t* counts, const float* loss, const float* loss_grad,
+                                 const void* workspace, size_t workspace_bytes) {
+  return check_route_groups(4, logits_f32, M, E, K, {groups, top_groups, group_top}, score, select_bias, token_mask,
+                            ids, weights, counts, loss, loss_grad, workspace, workspace_bytes);
 }
 
 int q4_route_backward(const void* logits_bf16, int64_t M, int64_t E, int64_t K, int score, int renormalize,

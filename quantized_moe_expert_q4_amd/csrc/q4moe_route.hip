@@ -147,6 +147,9 @@ __device__ __forceinline__ uint64_t order_key(double v) {
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
+__device__ __forceinline__ double key_value(uint64_t k) {
+  return __longlong_as_double((long long)(k ^ ((k >> 63) ? 0x8000000000000000ull : ~0ull)));
+}
 
 // The K experts of highest key, best first, ties to the lowest index, then -1,
 // into the group's out[0..K).  Keys are used up.  With `watch` (keys of 32
@@ -206,10 +209,78 @@ __device__ __forceinline__ void scores(const float (&x)[VPT], int sigmoid, T (&s
   sum = 1;
 }
 
-// The choice by score plus bias in double precision, for one token by a whole wave.
-template <int VPT>
+// The two highest keys of a group of experts (0 where there is none).
+template <class Key>
+struct BestTwo {
+  Key a, b;
+};
+template <class Key>
+__device__ __forceinline__ void add_key(BestTwo<Key>& t, decltype(t.a) k) {
+  const Key less = k < t.a ? k : t.a;
+  t.b = less > t.b ? less : t.b;
+  t.a = k > t.a ? k : t.a;
+}
+
+// What ranks a group: the sum of its `top` best keys' values (NaN if one is, so
+// that it ranks first; 0 without an expert to choose).  Two of the lowest F32,
+// as biases used as masks give them, do not add up to "none".
+__device__ __forceinline__ uint32_t group_key(BestTwo<uint32_t> t, int top) {
+  const float sum = key_value(t.a) + (top == 2 && t.b ? key_value(t.b) : 0.0f);
+  return t.a ? order_key(sum < -__FLT_MAX__ ? -__FLT_MAX__ : sum) : 0u;
+}
+__device__ __forceinline__ uint64_t group_key(BestTwo<uint64_t> t, int top) {
+  return t.a ? order_key(key_value(t.a) + (top == 2 && t.b ? key_value(t.b) : 0.0)) : 0ull;
+}
+
+// e / size by a product: exact for e < 1024 and size <= 1024 (magic = ceil(2^20
+// / size)).  Padding experts have higher groups, and keys of 0 whatever the mask says.
+struct GroupOf {
+  uint32_t magic;
+  __device__ explicit GroupOf(int size) : magic(((1u << 20) + (uint32_t)size - 1) / (uint32_t)size) {}
+  __device__ __forceinline__ int operator()(int e) const { return (int)(((uint32_t)e * magic) >> 20); }
+};
+
+// The token's kept groups as a mask: the top_groups highest of the keys rank[0
+// .. groups), ties to the lowest index, of those that have an expert to choose.
+// Each lane ranks the groups l, l + L, ..: a key's place is the number of keys
+// before it.  Sets `close` where F32 (keys of 32 bits, `watch`) cannot tell the
+// last one kept from the first one left out; the order within has no effect.
+template <int L, class Key>
+__device__ __forceinline__ uint64_t keep_groups(const Key* rank, int groups, int top_groups, int l, bool watch,
+                                                bool& close) {
+  uint64_t mask = 0;
+  Key last = 0, next = 0;
+  for (int g = l; g < groups; g += L) {
+    const Key mine = rank[g];
+    int place = 0;
+    for (int j = 0; j < groups; ++j) {
+      const Key other = rank[j];
+      place += other > mine || (other == mine && j < g);
+    }
+    if (mine && place < top_groups) mask |= 1ull << g;
+    last = place == top_groups - 1 ? mine : last;
+    next = place == top_groups ? mine : next;
+  }
+  mask = group_join<L>(mask, [](uint64_t a, uint64_t b) { return a | b; });
+  if constexpr (sizeof(Key) == 4) {
+    if (watch) {
+      last = group_max<L>(last);
+      next = group_max<L>(next);
+      // a sum of two scores differs by less than 64 roundings (2^-18) from what
+      // it should, those with biases by two half steps more
+      const float a = key_value(last);
+      close = last && next && !(a - key_value(next) > 0x1p-18f + 0x1p-21f * fabsf(a));
+    }
+  }
+  return mask;
+}
+
+// The choice in double precision, for one token by a whole wave: by score plus
+// bias, or by logit; with groups those are ranked in double too (`rank`, 64
+// keys of the wave's LDS).
+template <int VPT, bool GROUPED>
 __device__ __forceinline__ void choose_exact(const RouteParams& p, __amdgpu_buffer_rsrc_t src, uint32_t row, int lane,
-                                             int* out) {
+                                             uint64_t* rank, int* out) {
   float x[VPT], bias[VPT];
   load_row<64, VPT>(src, p.lf32, row, p.E, lane, x);
   load_experts<64, VPT>(p.bias, p.E, lane, bias);
@@ -220,6 +291,30 @@ __device__ __forceinline__ void choose_exact(const RouteParams& p, __amdgpu_buff
   for (int v = 0; v < VPT; ++v) {
     key[v] = order_key(s[v] + (double)bias[v]);
     key[v] = x[v] == -__builtin_inff() ? 0ull : key[v];
+  }
+  if constexpr (GROUPED) {
+    const int size = p.E / p.groups;
+    const GroupOf group_of(size);
+    for (int g = 0; g < p.groups; ++g) {
+      BestTwo<uint64_t> two = {0, 0};
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) add_key(two, group_of(v * 64 + lane) == g ? key[v] : 0ull);
+      two = group_join<64>(two, [](BestTwo<uint64_t> a, BestTwo<uint64_t> b) {
+        add_key(a, b.a);
+        add_key(a, b.b);
+        return a;
+      });
+      if (lane == 0) rank[g] = group_key(two, p.group_top);
+    }
+    wave_sync();
+    bool close;
+    const uint64_t keep = keep_groups<64>(rank, p.groups, p.top_groups, lane, false, close);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (!p.bias) key[v] = order_key((double)x[v]);
+      key[v] = (keep >> (group_of(v * 64 + lane) & 63)) & 1 ? key[v] : 0ull;
+    }
+    wave_sync();
   }
   choose<64, VPT>(key, p.K, lane, false, out);
 }
@@ -249,7 +344,9 @@ struct Partials {
 // STATS: with the batch statistics (p.partials).  They have kernels of their own
 // for the registers of their sums: with them 257..512 experts take 141, which
 // would leave the call without statistics one work-group a CU instead of two.
-template <int L, int VPT, bool STATS>
+// GROUPED: a token's experts come from its best groups.  Groups are ranked from
+// LDS, where a lane finds the experts of a group side by side.
+template <int L, int VPT, bool STATS, bool GROUPED>
 __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
   constexpr int G = 64 / L;          // tokens of a wave
   constexpr int kRow = L * VPT + 16; // floats of a token's scores in LDS (the four tokens on different banks)
@@ -257,6 +354,8 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
   __shared__ int s_pick[kWaves][G][kRouteMaxTopK];
   __shared__ int s_count[STATS ? L * VPT : 1];
   __shared__ int s_tokens;
+  __shared__ uint64_t s_rank[GROUPED ? kWaves : 1][kRouteMaxGroups];        // of the choice in double
+  __shared__ uint32_t s_rank32[GROUPED ? kWaves : 1][G][kRouteMaxGroups];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l = lane % L, group = lane / L;
@@ -284,17 +383,47 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
     load_row<L, VPT>(src, p.lf32, (uint32_t)group * pitch, p.E, l, x);
     scores<L, VPT, float>(x, p.sigmoid, s, sum);
     uint32_t key[VPT];
+    bool close_groups = false;
+    if constexpr (GROUPED) {
+      // one best expert by its logit, where no bias changes that order; else by score (plus bias)
+      const bool by_logit = !p.bias && p.group_top == 1;
+      const int size = p.E / p.groups;
+      const GroupOf group_of(size);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      score[v * L + l] = s[v];
-      key[v] = order_key(p.bias ? s[v] + bias[v] : x[v]);
-      key[v] = on && x[v] != -__builtin_inff() ? key[v] : 0u;
+      for (int v = 0; v < VPT; ++v) {          // the keys stand where the scores will
+        const uint32_t k = order_key(by_logit ? x[v] : s[v] + bias[v]);
+        score[v * L + l] = __uint_as_float(on && x[v] != -__builtin_inff() ? k : 0u);
+      }
+      wave_sync();
+      uint32_t* const rank = s_rank32[wave][group];
+      for (int g = l; g < p.groups; g += L) {
+        BestTwo<uint32_t> two = {0, 0};
+        for (int i = 0; i < size; ++i) add_key(two, __float_as_uint(score[g * size + i]));
+        rank[g] = group_key(two, p.group_top);
+      }
+      wave_sync();
+      const uint64_t keep = keep_groups<L>(rank, p.groups, p.top_groups, l, !by_logit, close_groups);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        key[v] = order_key(p.bias ? s[v] + bias[v] : x[v]);
+        key[v] = on && x[v] != -__builtin_inff() && ((keep >> (group_of(v * L + l) & 63)) & 1) ? key[v] : 0u;
+        score[v * L + l] = s[v];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        score[v * L + l] = s[v];
+        key[v] = order_key(p.bias ? s[v] + bias[v] : x[v]);
+        key[v] = on && x[v] != -__builtin_inff() ? key[v] : 0u;
+      }
     }
-    const bool close = choose<L, VPT>(key, p.K, l, p.bias != nullptr, pick);
+    const bool close = choose<L, VPT>(key, p.K, l, p.bias != nullptr, pick) || close_groups;
     // neighbours that F32 cannot tell apart: the same choice in double
     const uint64_t doubt = __ballot(close);
     for (int g = 0; g < G && doubt; ++g)
-      if ((doubt >> (g * L)) & 1) choose_exact<(L * VPT + 63) / 64>(p, src, (uint32_t)g * pitch, lane, s_pick[wave][g]);
+      if ((doubt >> (g * L)) & 1)
+        choose_exact<(L * VPT + 63) / 64, GROUPED>(p, src, (uint32_t)g * pitch, lane, s_rank[GROUPED ? wave : 0],
+                                                   s_pick[wave][g]);
     wave_sync();
     const bool here = pick[0] >= 0;
     float total = 1.0f;
@@ -536,8 +665,10 @@ hipError_t run(const void* const (&kernels)[10], const P& p, int blocks, hipStre
 // A kernel's variants by lanes of a token and experts of a lane.
 #define Q4_ROUTE_KERNELS(k) \
   {k(16, 1), k(16, 2), k(16, 4), k(16, 8), k(16, 16), k(64, 1), k(64, 2), k(64, 4), k(64, 8), k(64, 16)}
-#define Q4_ROUTE_PLAIN(L, VPT) reinterpret_cast<const void*>(&route_kernel<L, VPT, false>)
-#define Q4_ROUTE_STATS(L, VPT) reinterpret_cast<const void*>(&route_kernel<L, VPT, true>)
+#define Q4_ROUTE_PLAIN(L, VPT) reinterpret_cast<const void*>(&route_kernel<L, VPT, false, false>)
+#define Q4_ROUTE_STATS(L, VPT) reinterpret_cast<const void*>(&route_kernel<L, VPT, true, false>)
+#define Q4_ROUTE_GROUPS(L, VPT) reinterpret_cast<const void*>(&route_kernel<L, VPT, false, true>)
+#define Q4_ROUTE_GROUPS_STATS(L, VPT) reinterpret_cast<const void*>(&route_kernel<L, VPT, true, true>)
 #define Q4_ROUTE_BACKWARD(L, VPT) reinterpret_cast<const void*>(&route_backward_kernel<L, VPT>)
 
 }  // namespace
@@ -553,10 +684,12 @@ size_t route_partial_bytes(int64_t M, int64_t E) {
 hipError_t launch_route(const RouteParams& p, hipStream_t stream) {
   static const void* const plain[10] = Q4_ROUTE_KERNELS(Q4_ROUTE_PLAIN);
   static const void* const stats[10] = Q4_ROUTE_KERNELS(Q4_ROUTE_STATS);
+  static const void* const groups[10] = Q4_ROUTE_KERNELS(Q4_ROUTE_GROUPS);
+  static const void* const groups_stats[10] = Q4_ROUTE_KERNELS(Q4_ROUTE_GROUPS_STATS);
   const int all = token_blocks(p.M, p.E);
-  if (!p.partials) return run(plain, p, all < 65536 ? all : 65536, stream);
+  if (!p.partials) return run(p.groups ? groups : plain, p, all < 65536 ? all : 65536, stream);
   const int blocks = stat_blocks(p.M, p.E);
-  const hipError_t e = run(stats, p, blocks, stream);
+  const hipError_t e = run(p.groups ? groups_stats : stats, p, blocks, stream);
   if (e != hipSuccess) return e;
   RouteParams q = p;
   int nb = blocks;

@@ -1,0 +1,55 @@
+"""Plain 64-bit forms (numpy) of the router over groups, the adapters and the
+linear's gradient, written from their definitions in include/q4moe.h, with the
+magnitudes the tolerances scale with."""
+import numpy as np
+
+import layer_reference as ref
+
+
+def kept_groups(logits, groups, top_groups, group_top, score, bias):
+    """The kept groups of one token's logits [E], in 64 bits."""
+    l = np.asarray(logits, np.float64)
+    E = l.size
+    if bias is None and group_top == 1:
+        key = l.copy()
+    else:
+        s, _ = ref.scores(l, score)
+        key = s + (0.0 if bias is None else np.asarray(bias, np.float64))
+    key = np.where(l == -np.inf, -np.inf, key)
+    rank = []
+    for g in range(groups):
+        part = key[g * (E // groups):(g + 1) * (E // groups)]
+        part = sorted((v for v in part if not v == -np.inf), key=lambda v: (not np.isnan(v), -v))[:group_top]
+        rank.append((sum(part), g) if part else None)
+    order = sorted((r for r in rank if r is not None), key=lambda r: (not np.isnan(r[0]), -r[0], r[1]))
+    return [g for _, g in order[:top_groups]]
+
+
+def route_groups(logits, K, groups, top_groups, group_top, score, renormalize=False, scale=1.0, bias=None, mask=None):
+    """As layer_reference.route: the experts of the other groups are left out of
+    the choice (their logits taken as -inf there), not out of the scores."""
+    M, E = logits.shape
+    ids = np.full((M, K), -1, np.int64)
+    weights, counts, sums, tokens = np.zeros((M, K)), np.zeros(E, np.int64), np.zeros(E), 0
+    size = E // groups
+    for t in range(M):
+        l = np.asarray(logits[t], np.float64)
+        if (mask is not None and not mask[t]) or np.all(l == -np.inf):
+            continue
+        s, p = ref.scores(l, score)
+        key = l if bias is None else np.where(l == -np.inf, -np.inf, s + np.asarray(bias, np.float64))
+        keep = kept_groups(l, groups, top_groups, group_top, score, bias)
+        left = [e for g in sorted(keep) for e in range(g * size, (g + 1) * size) if not key[e] == -np.inf]
+        chosen = sorted(left, key=lambda e: (not np.isnan(key[e]), -key[e], e))[:K]
+        if not chosen:
+            continue
+        w = s[chosen]
+        if renormalize:
+            w = w / w.sum() if w.sum() != 0 else 0 * w
+        ids[t, :len(chosen)] = chosen
+        weights[t, :len(chosen)] = scale * w
+        counts[chosen] += 1
+        sums += p
+        tokens += 1
+    grad = E * counts / (K * float(tokens) ** 2) if tokens else np.zeros(E)
+    return ids, weights, counts, float((grad * sums).sum()), grad
