@@ -556,6 +556,40 @@ int q4_validate_linear_f32(const void *weights, const void *scales, const void *
                            int scale_type, int64_t group, const void *x_f32, int64_t M, int64_t N,
                            int64_t K, const void *out_f32);
 
+/*
+ * Gradient of the linear's input from that of its output (the weights are
+ * frozen):
+ *
+ *   d_x[m,k] = sum_n d_out[m,n] * W[n,k]
+ *
+ * W as above, from the same weights, scales, biases and group.  Sums are F32;
+ * d_x is rounded once to its type.  Float rows are multiplied with W rounded to
+ * F32, bf16 rows with W rounded to bf16 (as a bf16 matrix of the weights would
+ * hold it: 2^-8 relative to each weight at most, on top of the output's own).
+ *   d_out      device, [M][N], aligned to its type; d_x device, [M][K], 16-byte
+ *              aligned.
+ *   workspace  device, 256-byte aligned, q4_linear_backward_workspace_bytes(M,
+ *              N, K) bytes, which fall with none of the sizes; its contents on
+ *              entry are ignored.  Calls that share it must not overlap in time.
+ * Limits: those of q4_linear.
+ */
+size_t q4_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int q4_linear_backward(const void *weights, const void *scales, const void *biases, int scale_type,
+                       int64_t group, const void *d_out_bf16, int64_t M, int64_t N, int64_t K,
+                       void *d_x_bf16, void *workspace, size_t workspace_bytes, q4_stream_t stream);
+int q4_linear_backward_f32(const void *weights, const void *scales, const void *biases,
+                           int scale_type, int64_t group, const void *d_out_f32, int64_t M,
+                           int64_t N, int64_t K, void *d_x_f32, void *workspace,
+                           size_t workspace_bytes, q4_stream_t stream);
+int q4_validate_linear_backward(const void *weights, const void *scales, const void *biases,
+                                int scale_type, int64_t group, const void *d_out_bf16, int64_t M,
+                                int64_t N, int64_t K, const void *d_x_bf16, const void *workspace,
+                                size_t workspace_bytes);
+int q4_validate_linear_backward_f32(const void *weights, const void *scales, const void *biases,
+                                    int scale_type, int64_t group, const void *d_out_f32, int64_t M,
+                                    int64_t N, int64_t K, const void *d_x_f32, const void *workspace,
+                                    size_t workspace_bytes);
+
 /* Router scores: softmax over the experts, or the sigmoid of each logit. */
 enum { Q4_SCORE_SOFTMAX = 0, Q4_SCORE_SIGMOID = 1 };
 

@@ -35,6 +35,8 @@ from ._lib import (  # noqa: F401
     validate_down_grouped,
     stream_read,
     linear,
+    linear_backward,
+    linear_backward_workspace_bytes,
     route,
     route_groups,
     route_backward,
@@ -42,6 +44,7 @@ from ._lib import (  # noqa: F401
     combine,
     combine_backward,
     validate_linear,
+    validate_linear_backward,
     validate_route,
     validate_route_groups,
     validate_route_backward,

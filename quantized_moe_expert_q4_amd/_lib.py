@@ -158,6 +158,9 @@ _INT, _F32 = ctypes.c_int, ctypes.c_float
 for _suffix in ("", "_f32"):
     _SIGNATURES["q4_linear" + _suffix] = (_INT, [_P, _P, _P, _INT, _I64, _P, _I64, _I64, _I64, _P, _P])
     _SIGNATURES["q4_validate_linear" + _suffix] = (_INT, [_P, _P, _P, _INT, _I64, _P, _I64, _I64, _I64, _P])
+    _SIGNATURES["q4_linear_backward" + _suffix] = (_INT, [_P, _P, _P, _INT, _I64, _P, _I64, _I64, _I64, _P, _P, _SZ, _P])
+    _SIGNATURES["q4_validate_linear_backward" + _suffix] = (_INT, [_P, _P, _P, _INT, _I64, _P, _I64, _I64, _I64, _P, _P,
+                                                                   _SZ])
     _SIGNATURES["q4_route" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P, _P, _P,
                                                 _SZ, _P])
     _SIGNATURES["q4_route_groups" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _INT, _F32, _P, _P,
@@ -169,6 +172,7 @@ for _suffix in ("", "_f32"):
     _SIGNATURES["q4_validate_route_backward" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P])
     _SIGNATURES["q4_combine" + _suffix] = (_INT, [_P, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P])
     _SIGNATURES["q4_combine_backward" + _suffix] = (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P])
+_SIGNATURES["q4_linear_backward_workspace_bytes"] = (_SZ, [_I64, _I64, _I64])
 _SIGNATURES["q4_route_workspace_bytes"] = (_SZ, [_I64, _I64])
 _SIGNATURES["q4_validate_combine"] = (_INT, [_P, _P, _P, _I64, _P, _I64, _I64, _I64, _P])
 _SIGNATURES["q4_validate_combine_backward"] = (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P])
@@ -514,6 +518,35 @@ def validate_linear(weights, scales, x, M: int, N: int, K: int, group: int, out,
     return _fn(load(), "q4", "validate_linear", xdtype)(
         _ptr(weights), _ptr(scales), _ptr(biases), _SCALE_TYPES[_scale_type(scales, scale_dtype)], group, _ptr(x), M, N, K,
         _ptr(out))
+
+
+def linear_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().q4_linear_backward_workspace_bytes(M, N, K))
+
+
+def linear_backward(weights, scales, d_out, M: int, N: int, K: int, group: int, d_x, workspace, workspace_bytes: int,
+                    biases=None, stream=None, xdtype: str = "bf16", scale_dtype: Optional[str] = None) -> None:
+    """Enqueue the gradient of the linear's input (see q4_linear_backward in
+    include/q4moe.h): ``d_x`` [M, K] from ``d_out`` [M, N], both in ``xdtype``,
+    and the weights, scales and biases of :func:`linear`."""
+    fn = _fn(load(), "q4", "linear_backward", xdtype)
+    xt = _XDTYPE_NAMES[xdtype]
+    st = _scale_type(scales, scale_dtype)
+    n_scales = N * -(-K // group) if group in (32, 64, 128) else 0     # other groups: the library refuses the call
+    _args(("weights", weights, "uint8", N * (K // 2)), ("scales", scales, st, n_scales),
+          ("biases", biases, st, n_scales), ("d_out", d_out, xt, M * N), ("d_x", d_x, xt, M * K),
+          ("workspace", workspace, "uint8", workspace_bytes))
+    _check(fn(_ptr(weights), _ptr(scales), _ptr(biases), _SCALE_TYPES[st], group, _ptr(d_out), M, N, K, _ptr(d_x),
+              _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def validate_linear_backward(weights, scales, d_out, M: int, N: int, K: int, group: int, d_x, workspace,
+                             workspace_bytes: int, biases=None, xdtype: str = "bf16",
+                             scale_dtype: Optional[str] = None) -> int:
+    """Host-only argument check of the linear's gradient; returns the status."""
+    return _fn(load(), "q4", "validate_linear_backward", xdtype)(
+        _ptr(weights), _ptr(scales), _ptr(biases), _SCALE_TYPES[_scale_type(scales, scale_dtype)], group, _ptr(d_out), M,
+        N, K, _ptr(d_x), _ptr(workspace), workspace_bytes)
 
 
 def route_workspace_bytes(M: int, E: int) -> int:

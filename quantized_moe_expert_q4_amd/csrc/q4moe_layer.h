@@ -20,6 +20,19 @@ struct LinearParams {
   int scale_f32, xf32;
 };
 
+// d_x[m][k] = sum_n d_out[m][n] W[n][k] for the weights of the linear.
+struct LinearBackParams {
+  const uint8_t* w;       // as LinearParams
+  const void* scales;
+  const void* biases;
+  const void* d_out;      // [M][N], bf16 or float
+  void* d_x;              // [M][K], the type of d_out
+  float* partials;        // workspace
+  int M, N, K;
+  int group, groups;
+  int scale_f32, xf32;
+};
+
 // Router: logits [M][E] to the K chosen ids and weights of each token and,
 // with `partials`, the batch statistics.
 struct RouteParams {
@@ -65,6 +78,10 @@ struct CombineParams {
 };
 
 hipError_t launch_linear(const LinearParams& p, hipStream_t stream);
+
+// Bytes of the workspace of the linear's gradient for M tokens.
+size_t linear_back_partial_bytes(int64_t M, int64_t K);
+hipError_t launch_linear_backward(const LinearBackParams& p, hipStream_t stream);
 
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopK = 64;

@@ -67,6 +67,46 @@ int run_linear(bool f32, const void* w, const void* scales, const void* biases, 
   return launched(q4::launch_linear(p, reinterpret_cast<hipStream_t>(stream)));
 }
 
+int check_workspace(const void* ws, size_t ws_bytes, size_t need, const char* too_small) {
+  if (!ws) return report(Q4_ERR_WORKSPACE, "the call needs a workspace");
+  if (!aligned(ws, 256)) return report(Q4_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  if (ws_bytes < need) return report(Q4_ERR_WORKSPACE, too_small);
+  return Q4_OK;
+}
+
+// The same sizes and tensors as the linear: d_out in the place of its output, d_x in that of x.
+int check_linear_backward(bool f32, const void* w, const void* scales, const void* biases, int scale_type,
+                          int64_t group, const void* d_out, int64_t M, int64_t N, int64_t K, const void* d_x,
+                          const void* ws, size_t ws_bytes) {
+  const int rc = check_linear(f32, w, scales, biases, scale_type, group, d_x, M, N, K, d_out);
+  if (rc) return rc;
+  const int space = check_workspace(ws, ws_bytes, q4_linear_backward_workspace_bytes(M, N, K),
+                                    "workspace is smaller than q4_linear_backward_workspace_bytes()");
+  return space ? space : report(Q4_OK, "");
+}
+
+int run_linear_backward(bool f32, const void* w, const void* scales, const void* biases, int scale_type, int64_t group,
+                        const void* d_out, int64_t M, int64_t N, int64_t K, void* d_x, void* ws, size_t ws_bytes,
+                        q4_stream_t stream) {
+  const int rc = check_linear_backward(f32, w, scales, biases, scale_type, group, d_out, M, N, K, d_x, ws, ws_bytes);
+  if (rc) return rc;
+  q4::LinearBackParams p{};
+  p.w = static_cast<const uint8_t*>(w);
+  p.scales = scales;
+  p.biases = biases;
+  p.d_out = d_out;
+  p.d_x = d_x;
+  p.partials = static_cast<float*>(ws);
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.group = (int)group;
+  p.groups = (int)((K + group - 1) / group);
+  p.scale_f32 = scale_type == Q4_SCALE_F32;
+  p.xf32 = f32;
+  return launched(q4::launch_linear_backward(p, reinterpret_cast<hipStream_t>(stream)));
+}
+
 int check_route_sizes(int64_t M, int64_t E, int64_t K, int score) {
   if (M < 1) return report(Q4_ERR_INVALID_ARGUMENT, "router requires logits [M,E] with M >= 1");
   if (E < 1) return report(Q4_ERR_INVALID_ARGUMENT, "number of experts must be a positive integer");
@@ -301,6 +341,41 @@ int q4_validate_linear(const void* weights, const void* scales, const void* bias
 int q4_validate_linear_f32(const void* weights, const void* scales, const void* biases, int scale_type, int64_t group,
                            const void* x_f32, int64_t M, int64_t N, int64_t K, const void* out_f32) {
   return check_linear(true, weights, scales, biases, scale_type, group, x_f32, M, N, K, out_f32);
+}
+
+size_t q4_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || N < 1 || K < 8 || K % 8 != 0 || M > kMaxRows || K > kMaxK ||
+      (uint64_t)N > kMaxWeightBytes / (uint64_t)(K / 2))
+    return 0;
+  return q4::linear_back_partial_bytes(M, K);
+}
+
+int q4_linear_backward(const void* weights, const void* scales, const void* biases, int scale_type, int64_t group,
+                       const void* d_out_bf16, int64_t M, int64_t N, int64_t K, void* d_x_bf16, void* workspace,
+                       size_t workspace_bytes, q4_stream_t stream) {
+  return run_linear_backward(false, weights, scales, biases, scale_type, group, d_out_bf16, M, N, K, d_x_bf16, workspace,
+                             workspace_bytes, stream);
+}
+
+int q4_linear_backward_f32(const void* weights, const void* scales, const void* biases, int scale_type, int64_t group,
+                           const void* d_out_f32, int64_t M, int64_t N, int64_t K, void* d_x_f32, void* workspace,
+                           size_t workspace_bytes, q4_stream_t stream) {
+  return run_linear_backward(true, weights, scales, biases, scale_type, group, d_out_f32, M, N, K, d_x_f32, workspace,
+                             workspace_bytes, stream);
+}
+
+int q4_validate_linear_backward(const void* weights, const void* scales, const void* biases, int scale_type,
+                                int64_t group, const void* d_out_bf16, int64_t M, int64_t N, int64_t K,
+                                const void* d_x_bf16, const void* workspace, size_t workspace_bytes) {
+  return check_linear_backward(false, weights, scales, biases, scale_type, group, d_out_bf16, M, N, K, d_x_bf16,
+                               workspace, workspace_bytes);
+}
+
+int q4_validate_linear_backward_f32(const void* weights, const void* scales, const void* biases, int scale_type,
+                                    int64_t group, const void* d_out_f32, int64_t M, int64_t N, int64_t K,
+                                    const void* d_x_f32, const void* workspace, size_t workspace_bytes) {
+  return check_linear_backward(true, weights, scales, biases, scale_type, group, d_out_f32, M, N, K, d_x_f32, workspace,
+                               workspace_bytes);
 }
 
 size_t q4_route_workspace_bytes(int64_t M, int64_t E) {

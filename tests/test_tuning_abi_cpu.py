@@ -33,3 +33,35 @@ def test_route_groups_accepts(kw):
 def test_route_groups_refuses(kw, status):
     got, message = _groups(**kw)
     assert got == status and message
+
+
+def _back(xdtype="bf16", **kw):
+    a = dict(weights=W, scales=S, d_out=X, M=1, N=4096, K=4096, group=64, d_x=OUT, workspace=WS, workspace_bytes=1 << 26,
+             biases=None, scale_dtype="bfloat16")
+    a.update(kw)
+    return q4.validate_linear_backward(xdtype=xdtype, **a), q4.last_error()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(biases=B), dict(M=65535), dict(K=8), dict(K=65536), dict(N=1), dict(group=32),
+                                dict(group=128, K=4104), dict(xdtype="f32"), dict(scale_dtype="float32"),
+                                dict(d_out=X + 2), dict(d_out=X + 4, xdtype="f32")])
+def test_linear_backward_accepts(kw):
+    assert _back(**kw) == (0, "")
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=0), INVALID), (dict(N=0), INVALID), (dict(K=0), INVALID), (dict(K=4100), INVALID), (dict(group=16), UNSUPPORTED),
+    (dict(M=65536), UNSUPPORTED), (dict(K=65544), UNSUPPORTED), (dict(N=1 << 20, K=4096), UNSUPPORTED),
+    (dict(N=1 << 62), UNSUPPORTED), (dict(weights=None), INVALID), (dict(scales=None), INVALID), (dict(d_out=None), INVALID),
+    (dict(d_x=None), INVALID), (dict(weights=W + 8), ALIGN), (dict(d_x=OUT + 8), ALIGN), (dict(d_out=X + 1), ALIGN),
+    (dict(d_out=X + 2, xdtype="f32"), ALIGN), (dict(scales=S + 1), ALIGN), (dict(biases=B + 1), ALIGN),
+    (dict(workspace=None), WORKSPACE), (dict(workspace=WS + 128), ALIGN), (dict(workspace_bytes=0), WORKSPACE)])
+def test_linear_backward_refuses(kw, status):
+    got, message = _back(**kw)
+    assert got == status and message
+
+
+def test_linear_backward_workspace():
+    assert q4.linear_backward_workspace_bytes(1, 1, 8) % 256 == 0
+    for M, N, K in ((0, 8, 8), (1, 0, 8), (1, 8, 0), (1, 8, 12), (65536, 8, 8), (1, 1 << 40, 4096), (1, 8, 65544)):
+        assert q4.linear_backward_workspace_bytes(M, N, K) == 0

@@ -53,3 +53,17 @@ def route_groups(logits, K, groups, top_groups, group_top, score, renormalize=Fa
         tokens += 1
     grad = E * counts / (K * float(tokens) ** 2) if tokens else np.zeros(E)
     return ids, weights, counts, float((grad * sums).sum()), grad
+
+
+def dense_weights(weights, scales, biases, group, N, K):
+    """W [N, K] in 64 bits."""
+    q = ref.unpack_q4(weights, N, K).astype(np.float64)
+    wide = lambda a: np.repeat(np.asarray(a, np.float64), group, axis=1)[:, :K]
+    return wide(scales) * (q - 8) if biases is None else wide(scales) * q + wide(biases)
+
+
+def linear_backward(weights, scales, biases, group, d_out, N, K):
+    """(d_x [M, K], magnitude [M, K])."""
+    W = dense_weights(weights, scales, biases, group, N, K)
+    d = np.asarray(d_out, np.float64)
+    return d @ W, np.abs(d) @ np.abs(W)
