@@ -590,6 +590,100 @@ int q4_validate_linear_backward_f32(const void *weights, const void *scales, con
                                     int64_t N, int64_t K, const void *d_x_f32, const void *workspace,
                                     size_t workspace_bytes);
 
+/*
+ * Low-rank adapters of many requests beside a projection they share.  Row t
+ * has the adapter i = adapter_ids[t], or none where that lies outside [0,
+ * num_adapters):
+ *
+ *   hidden[t,:] = A_i x[t,:]                       (0 without an adapter)
+ *   out[t,:]    = base[t,:] + scales[i] * B_i hidden[t,:]
+ *
+ * Sums and the hidden values are F32; out is rounded once.  bf16 calls take the
+ * hidden values into the second product with 16 bits (2^-16 relative at most), a
+ * 256th of the output's own rounding.  A row's result takes nothing from the rows and adapters of others, whatever those
+ * hold.  Rows of one adapter need not stand together, but are read together
+ * only within 256 neighbouring rows.
+ *   a, b   device, [num_adapters][R][K] and [num_adapters][N][R], 16-byte
+ *          aligned, in the type of the rows.  An adapter of lower rank is padded
+ *          with zeros.
+ *   x      device, [M][K], 16-byte aligned.
+ *   adapter_ids  device int32 [M], or NULL: every row has adapter 0.
+ *   scales device F32 [num_adapters], or NULL: 1.
+ *   base   device, [M][N], aligned to its type, or NULL: 0.  It may be out
+ *          itself: the output of q4_linear, for one.
+ *   out    device, [M][N], aligned to its type.
+ *   hidden device F32 [M][R], 16-byte aligned, or NULL: written for the
+ *          backward call.
+ *   workspace  device, 256-byte aligned, q4_adapter_workspace_bytes(M, N, K, R,
+ *          num_adapters) bytes, which fall with none of the sizes; contents on
+ *          entry are ignored.  Calls that share it must not overlap in time.
+ * Apart from base and out no two arguments may overlap.
+ * Limits: 1 <= M <= 65535, 1 <= N <= 2^20, 8 <= K <= 65536 with K % 8 == 0,
+ * 8 <= R <= 256 with R % 8 == 0, 1 <= num_adapters <= 65535.
+ */
+size_t q4_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t num_adapters);
+int q4_adapter(const void *a_bf16, const void *b_bf16, const void *x_bf16, int64_t M, int64_t N,
+               int64_t K, int64_t R, int64_t num_adapters, const int32_t *adapter_ids,
+               const float *scales, const void *base_bf16, void *out_bf16, float *hidden,
+               void *workspace, size_t workspace_bytes, q4_stream_t stream);
+int q4_adapter_f32(const void *a_f32, const void *b_f32, const void *x_f32, int64_t M, int64_t N,
+                   int64_t K, int64_t R, int64_t num_adapters, const int32_t *adapter_ids,
+                   const float *scales, const void *base_f32, void *out_f32, float *hidden,
+                   void *workspace, size_t workspace_bytes, q4_stream_t stream);
+int q4_validate_adapter(const void *a_bf16, const void *b_bf16, const void *x_bf16, int64_t M,
+                        int64_t N, int64_t K, int64_t R, int64_t num_adapters,
+                        const int32_t *adapter_ids, const float *scales, const void *base_bf16,
+                        const void *out_bf16, const float *hidden, const void *workspace,
+                        size_t workspace_bytes);
+int q4_validate_adapter_f32(const void *a_f32, const void *b_f32, const void *x_f32, int64_t M,
+                            int64_t N, int64_t K, int64_t R, int64_t num_adapters,
+                            const int32_t *adapter_ids, const float *scales, const void *base_f32,
+                            const void *out_f32, const float *hidden, const void *workspace,
+                            size_t workspace_bytes);
+
+/*
+ * Gradients of the adapters from d_out [M][N], for the rows t of each adapter i:
+ *
+ *   g[t,:]   = scales[i] * B_i^T d_out[t,:]        (F32)
+ *   d_x[t,:] = base[t,:] + A_i^T g[t,:]            (base alone without an adapter)
+ *   d_a_i    = sum_t g[t,:] x[t,:]^T               (F32 [num_adapters][R][K])
+ *   d_b_i    = scales[i] * sum_t d_out[t,:] hidden[t,:]^T   (F32 [num_adapters][N][R])
+ *
+ * bf16 calls take g into d_x with 16 bits; d_a and d_b are F32 throughout.  An
+ * adapter without rows gets zeros.  The forward call's base has the gradient
+ * d_out; this call's base is what reaches x another way (through the
+ * projection: q4_linear_backward) or NULL, and may be d_x itself.  Any of d_x,
+ * d_a and d_b may be NULL, not all; d_a needs x, d_b needs the hidden of the
+ * forward call.  The sums over the rows are in a fixed order: the same bits on
+ * every run.
+ *   x, hidden, base, d_x, d_a, d_b are 16-byte aligned, d_out to its type;
+ *   adapter_ids, scales, workspace and limits as in q4_adapter.
+ */
+int q4_adapter_backward(const void *d_out_bf16, const void *a_bf16, const void *b_bf16,
+                        const void *x_bf16, const float *hidden, int64_t M, int64_t N, int64_t K,
+                        int64_t R, int64_t num_adapters, const int32_t *adapter_ids,
+                        const float *scales, const void *base_bf16, void *d_x_bf16, float *d_a,
+                        float *d_b, void *workspace, size_t workspace_bytes, q4_stream_t stream);
+int q4_adapter_backward_f32(const void *d_out_f32, const void *a_f32, const void *b_f32,
+                            const void *x_f32, const float *hidden, int64_t M, int64_t N,
+                            int64_t K, int64_t R, int64_t num_adapters, const int32_t *adapter_ids,
+                            const float *scales, const void *base_f32, void *d_x_f32, float *d_a,
+                            float *d_b, void *workspace, size_t workspace_bytes,
+                            q4_stream_t stream);
+int q4_validate_adapter_backward(const void *d_out_bf16, const void *a_bf16, const void *b_bf16,
+                                 const void *x_bf16, const float *hidden, int64_t M, int64_t N,
+                                 int64_t K, int64_t R, int64_t num_adapters,
+                                 const int32_t *adapter_ids, const float *scales,
+                                 const void *base_bf16, const void *d_x_bf16, const float *d_a,
+                                 const float *d_b, const void *workspace, size_t workspace_bytes);
+int q4_validate_adapter_backward_f32(const void *d_out_f32, const void *a_f32, const void *b_f32,
+                                     const void *x_f32, const float *hidden, int64_t M, int64_t N,
+                                     int64_t K, int64_t R, int64_t num_adapters,
+                                     const int32_t *adapter_ids, const float *scales,
+                                     const void *base_f32, const void *d_x_f32, const float *d_a,
+                                     const float *d_b, const void *workspace,
+                                     size_t workspace_bytes);
+
 /* Router scores: softmax over the experts, or the sigmoid of each logit. */
 enum { Q4_SCORE_SOFTMAX = 0, Q4_SCORE_SIGMOID = 1 };
 

@@ -161,6 +161,10 @@ for _suffix in ("", "_f32"):
     _SIGNATURES["q4_linear_backward" + _suffix] = (_INT, [_P, _P, _P, _INT, _I64, _P, _I64, _I64, _I64, _P, _P, _SZ, _P])
     _SIGNATURES["q4_validate_linear_backward" + _suffix] = (_INT, [_P, _P, _P, _INT, _I64, _P, _I64, _I64, _I64, _P, _P,
                                                                    _SZ])
+    _SIGNATURES["q4_adapter" + _suffix] = (_INT, [_P, _P, _P] + [_I64] * 5 + [_P] * 6 + [_SZ, _P])
+    _SIGNATURES["q4_validate_adapter" + _suffix] = (_INT, [_P, _P, _P] + [_I64] * 5 + [_P] * 6 + [_SZ])
+    _SIGNATURES["q4_adapter_backward" + _suffix] = (_INT, [_P] * 5 + [_I64] * 5 + [_P] * 7 + [_SZ, _P])
+    _SIGNATURES["q4_validate_adapter_backward" + _suffix] = (_INT, [_P] * 5 + [_I64] * 5 + [_P] * 7 + [_SZ])
     _SIGNATURES["q4_route" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _INT, _INT, _F32, _P, _P, _P, _P, _P, _P, _P, _P,
                                                 _SZ, _P])
     _SIGNATURES["q4_route_groups" + _suffix] = (_INT, [_P, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _INT, _F32, _P, _P,
@@ -173,6 +177,7 @@ for _suffix in ("", "_f32"):
     _SIGNATURES["q4_combine" + _suffix] = (_INT, [_P, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P])
     _SIGNATURES["q4_combine_backward" + _suffix] = (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P])
 _SIGNATURES["q4_linear_backward_workspace_bytes"] = (_SZ, [_I64, _I64, _I64])
+_SIGNATURES["q4_adapter_workspace_bytes"] = (_SZ, [_I64] * 5)
 _SIGNATURES["q4_route_workspace_bytes"] = (_SZ, [_I64, _I64])
 _SIGNATURES["q4_validate_combine"] = (_INT, [_P, _P, _P, _I64, _P, _I64, _I64, _I64, _P])
 _SIGNATURES["q4_validate_combine_backward"] = (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P])
@@ -547,6 +552,62 @@ def validate_linear_backward(weights, scales, d_out, M: int, N: int, K: int, gro
     return _fn(load(), "q4", "validate_linear_backward", xdtype)(
         _ptr(weights), _ptr(scales), _ptr(biases), _SCALE_TYPES[_scale_type(scales, scale_dtype)], group, _ptr(d_out), M,
         N, K, _ptr(d_x), _ptr(workspace), workspace_bytes)
+
+
+def adapter_workspace_bytes(M: int, N: int, K: int, R: int, num_adapters: int) -> int:
+    return int(load().q4_adapter_workspace_bytes(M, N, K, R, num_adapters))
+
+
+def adapter(a, b, x, M: int, N: int, K: int, R: int, num_adapters: int, out, workspace, workspace_bytes: int,
+            adapter_ids=None, scales=None, base=None, hidden=None, stream=None, xdtype: str = "bf16") -> None:
+    """Enqueue the low-rank adapters of the rows of ``x`` [M, K] (see q4_adapter
+    in include/q4moe.h): ``out`` [M, N] = ``base`` + ``scales`` B A x with ``a``
+    [num_adapters, R, K] and ``b`` [num_adapters, N, R] of each row's id, all in
+    ``xdtype``; ``hidden`` (F32 [M, R]) keeps A x for the backward call."""
+    fn = _fn(load(), "q4", "adapter", xdtype)
+    xt = _XDTYPE_NAMES[xdtype]
+    _args(("a", a, xt, num_adapters * R * K), ("b", b, xt, num_adapters * N * R), ("x", x, xt, M * K),
+          ("adapter_ids", adapter_ids, "int32", M), ("scales", scales, "float32", num_adapters),
+          ("base", base, xt, M * N), ("out", out, xt, M * N), ("hidden", hidden, "float32", M * R),
+          ("workspace", workspace, "uint8", workspace_bytes))
+    _check(fn(_ptr(a), _ptr(b), _ptr(x), M, N, K, R, num_adapters, _ptr(adapter_ids), _ptr(scales), _ptr(base), _ptr(out),
+              _ptr(hidden), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def validate_adapter(a, b, x, M: int, N: int, K: int, R: int, num_adapters: int, out, workspace, workspace_bytes: int,
+                     adapter_ids=None, scales=None, base=None, hidden=None, xdtype: str = "bf16") -> int:
+    """Host-only argument check of the adapters; returns the status."""
+    return _fn(load(), "q4", "validate_adapter", xdtype)(
+        _ptr(a), _ptr(b), _ptr(x), M, N, K, R, num_adapters, _ptr(adapter_ids), _ptr(scales), _ptr(base), _ptr(out),
+        _ptr(hidden), _ptr(workspace), workspace_bytes)
+
+
+def adapter_backward(d_out, a, b, M: int, N: int, K: int, R: int, num_adapters: int, workspace, workspace_bytes: int,
+                     x=None, hidden=None, d_x=None, d_a=None, d_b=None, adapter_ids=None, scales=None, base=None,
+                     stream=None, xdtype: str = "bf16") -> None:
+    """Enqueue the gradients of the adapters (see q4_adapter_backward in
+    include/q4moe.h): ``d_x`` [M, K] in ``xdtype`` onto ``base``, ``d_a`` and
+    ``d_b`` in F32 in the shapes of ``a`` and ``b``, each when given; ``d_a``
+    needs ``x``, ``d_b`` the ``hidden`` of the forward call."""
+    fn = _fn(load(), "q4", "adapter_backward", xdtype)
+    xt = _XDTYPE_NAMES[xdtype]
+    _args(("d_out", d_out, xt, M * N), ("a", a, xt, num_adapters * R * K), ("b", b, xt, num_adapters * N * R),
+          ("x", x, xt, M * K), ("hidden", hidden, "float32", M * R), ("adapter_ids", adapter_ids, "int32", M),
+          ("scales", scales, "float32", num_adapters), ("base", base, xt, M * K), ("d_x", d_x, xt, M * K),
+          ("d_a", d_a, "float32", num_adapters * R * K), ("d_b", d_b, "float32", num_adapters * N * R),
+          ("workspace", workspace, "uint8", workspace_bytes))
+    _check(fn(_ptr(d_out), _ptr(a), _ptr(b), _ptr(x), _ptr(hidden), M, N, K, R, num_adapters, _ptr(adapter_ids),
+              _ptr(scales), _ptr(base), _ptr(d_x), _ptr(d_a), _ptr(d_b), _ptr(workspace), workspace_bytes,
+              _stream(stream)))
+
+
+def validate_adapter_backward(d_out, a, b, M: int, N: int, K: int, R: int, num_adapters: int, workspace,
+                              workspace_bytes: int, x=None, hidden=None, d_x=None, d_a=None, d_b=None, adapter_ids=None,
+                              scales=None, base=None, xdtype: str = "bf16") -> int:
+    """Host-only argument check of the adapters' gradients; returns the status."""
+    return _fn(load(), "q4", "validate_adapter_backward", xdtype)(
+        _ptr(d_out), _ptr(a), _ptr(b), _ptr(x), _ptr(hidden), M, N, K, R, num_adapters, _ptr(adapter_ids), _ptr(scales),
+        _ptr(base), _ptr(d_x), _ptr(d_a), _ptr(d_b), _ptr(workspace), workspace_bytes)
 
 
 def route_workspace_bytes(M: int, E: int) -> int:

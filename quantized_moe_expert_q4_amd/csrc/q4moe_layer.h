@@ -33,6 +33,36 @@ struct LinearBackParams {
   int scale_f32, xf32;
 };
 
+// out[t] = base[t] + s B h[t], h[t] = A x[t], with the adapter of row t.
+struct AdapterParams {
+  const void* a;              // [n][R][K], bf16 or float as every row below
+  const void* b;              // [n][N][R]
+  const void* x;              // [M][K]
+  const int32_t* ids;         // [M] or nullptr (adapter 0)
+  const float* scales;        // [n] or nullptr (1)
+  const void* base;           // [M][N] or nullptr
+  void* out;                  // [M][N]
+  float* hidden;              // [M][R] or nullptr
+  float* partial;             // workspace
+  int M, N, K, R, n, xf32;
+};
+
+struct AdapterBackwardParams {
+  const void* d_out;          // [M][N]
+  const void* a;
+  const void* b;
+  const void* x;              // [M][K] or nullptr without d_a
+  const float* hidden;        // [M][R] or nullptr without d_b
+  const int32_t* ids;
+  const float* scales;
+  const void* base;           // [M][K] or nullptr
+  void* d_x;                  // [M][K] or nullptr
+  float* d_a;                 // [n][R][K] or nullptr
+  float* d_b;                 // [n][N][R] or nullptr
+  float* partial;             // workspace
+  int M, N, K, R, n, xf32;
+};
+
 // Router: logits [M][E] to the K chosen ids and weights of each token and,
 // with `partials`, the batch statistics.
 struct RouteParams {
@@ -82,6 +112,11 @@ hipError_t launch_linear(const LinearParams& p, hipStream_t stream);
 // Bytes of the workspace of the linear's gradient for M tokens.
 size_t linear_back_partial_bytes(int64_t M, int64_t K);
 hipError_t launch_linear_backward(const LinearBackParams& p, hipStream_t stream);
+
+// Bytes of the workspace of both adapter calls.
+size_t adapter_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t n);
+hipError_t launch_adapter(const AdapterParams& p, hipStream_t stream);
+hipError_t launch_adapter_backward(const AdapterBackwardParams& p, hipStream_t stream);
 
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopK = 64;

@@ -14,6 +14,9 @@ constexpr int64_t kMaxK = 65536;
 constexpr int64_t kMaxRows = 65535;
 constexpr int64_t kMaxRouteTokens = 1ll << 24;
 constexpr uint64_t kMaxWeightBytes = (1ull << 31) - 16;
+constexpr int64_t kMaxAdapterColumns = 1ll << 20;
+constexpr int64_t kMaxRank = 256;
+constexpr int64_t kMaxAdapters = 65535;
 constexpr int64_t kMaxPairs = (1ll << 31) - 1;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -105,6 +108,119 @@ int run_linear_backward(bool f32, const void* w, const void* scales, const void*
   p.scale_f32 = scale_type == Q4_SCALE_F32;
   p.xf32 = f32;
   return launched(q4::launch_linear_backward(p, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int check_adapter_sizes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t num_adapters) {
+  if (M < 1) return report(Q4_ERR_INVALID_ARGUMENT, "adapter requires rows with M >= 1");
+  if (N < 1) return report(Q4_ERR_INVALID_ARGUMENT, "output columns must be a positive integer");
+  if (K < 1 || K % 8 != 0) return report(Q4_ERR_INVALID_ARGUMENT, "adapter needs K positive and divisible by 8");
+  if (R < 1 || R % 8 != 0) return report(Q4_ERR_INVALID_ARGUMENT, "rank must be positive and divisible by 8");
+  if (num_adapters < 1) return report(Q4_ERR_INVALID_ARGUMENT, "number of adapters must be a positive integer");
+  if (M > kMaxRows) return report(Q4_ERR_UNSUPPORTED, "more than 65535 rows per call is not supported");
+  if (N > kMaxAdapterColumns) return report(Q4_ERR_UNSUPPORTED, "more than 2^20 output columns is not supported");
+  if (K > kMaxK) return report(Q4_ERR_UNSUPPORTED, "K above 65536 is not supported");
+  if (R > kMaxRank) return report(Q4_ERR_UNSUPPORTED, "rank above 256 is not supported");
+  if (num_adapters > kMaxAdapters) return report(Q4_ERR_UNSUPPORTED, "more than 65535 adapters is not supported");
+  return Q4_OK;
+}
+
+int check_adapter_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t num_adapters, const void* ws,
+                            size_t ws_bytes) {
+  return check_workspace(ws, ws_bytes, q4::adapter_workspace(M, N, K, R, num_adapters),
+                         "workspace is smaller than q4_adapter_workspace_bytes()");
+}
+
+int check_adapter(bool f32, const void* a, const void* b, const void* x, int64_t M, int64_t N, int64_t K, int64_t R,
+                  int64_t num_adapters, const int32_t* ids, const float* scales, const void* base, const void* out,
+                  const float* hidden, const void* ws, size_t ws_bytes) {
+  const int rc = check_adapter_sizes(M, N, K, R, num_adapters);
+  if (rc) return rc;
+  if (!a || !b || !x || !out)
+    return report(Q4_ERR_INVALID_ARGUMENT, "adapters, x and output must be non-null device pointers");
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(x, 16))
+    return report(Q4_ERR_ALIGNMENT, "adapters and x must be 16-byte aligned");
+  if (!aligned(base, f32 ? 4 : 2) || !aligned(out, f32 ? 4 : 2))
+    return report(Q4_ERR_ALIGNMENT, "base and output must be aligned to their type");
+  if (!aligned(ids, 4) || !aligned(scales, 4)) return report(Q4_ERR_ALIGNMENT, "ids and scales must be 4-byte aligned");
+  if (!aligned(hidden, 16)) return report(Q4_ERR_ALIGNMENT, "hidden must be 16-byte aligned");
+  const int space = check_adapter_workspace(M, N, K, R, num_adapters, ws, ws_bytes);
+  return space ? space : report(Q4_OK, "");
+}
+
+int run_adapter(bool f32, const void* a, const void* b, const void* x, int64_t M, int64_t N, int64_t K, int64_t R,
+                int64_t num_adapters, const int32_t* ids, const float* scales, const void* base, void* out,
+                float* hidden, void* ws, size_t ws_bytes, q4_stream_t stream) {
+  const int rc = check_adapter(f32, a, b, x, M, N, K, R, num_adapters, ids, scales, base, out, hidden, ws, ws_bytes);
+  if (rc) return rc;
+  q4::AdapterParams p{};
+  p.a = a;
+  p.b = b;
+  p.x = x;
+  p.ids = ids;
+  p.scales = scales;
+  p.base = base;
+  p.out = out;
+  p.hidden = hidden;
+  p.partial = static_cast<float*>(ws);
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.R = (int)R;
+  p.n = (int)num_adapters;
+  p.xf32 = f32;
+  return launched(q4::launch_adapter(p, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int check_adapter_backward(bool f32, const void* d_out, const void* a, const void* b, const void* x,
+                           const float* hidden, int64_t M, int64_t N, int64_t K, int64_t R, int64_t num_adapters,
+                           const int32_t* ids, const float* scales, const void* base, const void* d_x,
+                           const float* d_a, const float* d_b, const void* ws, size_t ws_bytes) {
+  const int rc = check_adapter_sizes(M, N, K, R, num_adapters);
+  if (rc) return rc;
+  if (!d_out || !a || !b)
+    return report(Q4_ERR_INVALID_ARGUMENT, "the output's gradient and adapters must be non-null device pointers");
+  if (!d_x && !d_a && !d_b) return report(Q4_ERR_INVALID_ARGUMENT, "d_x, d_a or d_b must be given");
+  if (d_a && !x) return report(Q4_ERR_INVALID_ARGUMENT, "d_a needs x");
+  if (d_b && !hidden) return report(Q4_ERR_INVALID_ARGUMENT, "d_b needs hidden");
+  if (base && !d_x) return report(Q4_ERR_INVALID_ARGUMENT, "base is given without d_x");
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(x, 16))
+    return report(Q4_ERR_ALIGNMENT, "adapters and x must be 16-byte aligned");
+  if (!aligned(d_out, f32 ? 4 : 2))
+    return report(Q4_ERR_ALIGNMENT, "the output's gradient must be aligned to its type");
+  if (!aligned(base, 16) || !aligned(d_x, 16) || !aligned(d_a, 16) || !aligned(d_b, 16) || !aligned(hidden, 16))
+    return report(Q4_ERR_ALIGNMENT, "hidden, base and gradients must be 16-byte aligned");
+  if (!aligned(ids, 4) || !aligned(scales, 4)) return report(Q4_ERR_ALIGNMENT, "ids and scales must be 4-byte aligned");
+  const int space = check_adapter_workspace(M, N, K, R, num_adapters, ws, ws_bytes);
+  return space ? space : report(Q4_OK, "");
+}
+
+int run_adapter_backward(bool f32, const void* d_out, const void* a, const void* b, const void* x, const float* hidden,
+                         int64_t M, int64_t N, int64_t K, int64_t R, int64_t num_adapters, const int32_t* ids,
+                         const float* scales, const void* base, void* d_x, float* d_a, float* d_b, void* ws,
+                         size_t ws_bytes, q4_stream_t stream) {
+  const int rc = check_adapter_backward(f32, d_out, a, b, x, hidden, M, N, K, R, num_adapters, ids, scales, base, d_x,
+                                        d_a, d_b, ws, ws_bytes);
+  if (rc) return rc;
+  q4::AdapterBackwardParams p{};
+  p.d_out = d_out;
+  p.a = a;
+  p.b = b;
+  p.x = x;
+  p.hidden = hidden;
+  p.ids = ids;
+  p.scales = scales;
+  p.base = base;
+  p.d_x = d_x;
+  p.d_a = d_a;
+  p.d_b = d_b;
+  p.partial = static_cast<float*>(ws);
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.R = (int)R;
+  p.n = (int)num_adapters;
+  p.xf32 = f32;
+  return launched(q4::launch_adapter_backward(p, reinterpret_cast<hipStream_t>(stream)));
 }
 
 int check_route_sizes(int64_t M, int64_t E, int64_t K, int score) {
@@ -376,6 +492,75 @@ int q4_validate_linear_backward_f32(const void* weights, const void* scales, con
                                     const void* d_x_f32, const void* workspace, size_t workspace_bytes) {
   return check_linear_backward(true, weights, scales, biases, scale_type, group, d_out_f32, M, N, K, d_x_f32, workspace,
                                workspace_bytes);
+}
+
+size_t q4_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t num_adapters) {
+  if (check_adapter_sizes(M, N, K, R, num_adapters) != Q4_OK) return 0;
+  return q4::adapter_workspace(M, N, K, R, num_adapters);
+}
+
+int q4_adapter(const void* a_bf16, const void* b_bf16, const void* x_bf16, int64_t M, int64_t N, int64_t K, int64_t R,
+               int64_t num_adapters, const int32_t* adapter_ids, const float* scales, const void* base_bf16,
+               void* out_bf16, float* hidden, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
+  return run_adapter(false, a_bf16, b_bf16, x_bf16, M, N, K, R, num_adapters, adapter_ids, scales, base_bf16, out_bf16,
+                     hidden, workspace, workspace_bytes, stream);
+}
+
+int q4_adapter_f32(const void* a_f32, const void* b_f32, const void* x_f32, int64_t M, int64_t N, int64_t K, int64_t R,
+                   int64_t num_adapters, const int32_t* adapter_ids, const float* scales, const void* base_f32,
+                   void* out_f32, float* hidden, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
+  return run_adapter(true, a_f32, b_f32, x_f32, M, N, K, R, num_adapters, adapter_ids, scales, base_f32, out_f32, hidden,
+                     workspace, workspace_bytes, stream);
+}
+
+int q4_validate_adapter(const void* a_bf16, const void* b_bf16, const void* x_bf16, int64_t M, int64_t N, int64_t K,
+                        int64_t R, int64_t num_adapters, const int32_t* adapter_ids, const float* scales,
+                        const void* base_bf16, const void* out_bf16, const float* hidden, const void* workspace,
+                        size_t workspace_bytes) {
+  return check_adapter(false, a_bf16, b_bf16, x_bf16, M, N, K, R, num_adapters, adapter_ids, scales, base_bf16, out_bf16,
+                       hidden, workspace, workspace_bytes);
+}
+
+int q4_validate_adapter_f32(const void* a_f32, const void* b_f32, const void* x_f32, int64_t M, int64_t N, int64_t K,
+                            int64_t R, int64_t num_adapters, const int32_t* adapter_ids, const float* scales,
+                            const void* base_f32, const void* out_f32, const float* hidden, const void* workspace,
+                            size_t workspace_bytes) {
+  return check_adapter(true, a_f32, b_f32, x_f32, M, N, K, R, num_adapters, adapter_ids, scales, base_f32, out_f32,
+                       hidden, workspace, workspace_bytes);
+}
+
+int q4_adapter_backward(const void* d_out_bf16, const void* a_bf16, const void* b_bf16, const void* x_bf16,
+                        const float* hidden, int64_t M, int64_t N, int64_t K, int64_t R, int64_t num_adapters,
+                        const int32_t* adapter_ids, const float* scales, const void* base_bf16, void* d_x_bf16,
+                        float* d_a, float* d_b, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
+  return run_adapter_backward(false, d_out_bf16, a_bf16, b_bf16, x_bf16, hidden, M, N, K, R, num_adapters, adapter_ids,
+                              scales, base_bf16, d_x_bf16, d_a, d_b, workspace, workspace_bytes, stream);
+}
+
+int q4_adapter_backward_f32(const void* d_out_f32, const void* a_f32, const void* b_f32, const void* x_f32,
+                            const float* hidden, int64_t M, int64_t N, int64_t K, int64_t R, int64_t num_adapters,
+                            const int32_t* adapter_ids, const float* scales, const void* base_f32, void* d_x_f32,
+                            float* d_a, float* d_b, void* workspace, size_t workspace_bytes, q4_stream_t stream) {
+  return run_adapter_backward(true, d_out_f32, a_f32, b_f32, x_f32, hidden, M, N, K, R, num_adapters, adapter_ids,
+                              scales, base_f32, d_x_f32, d_a, d_b, workspace, workspace_bytes, stream);
+}
+
+int q4_validate_adapter_backward(const void* d_out_bf16, const void* a_bf16, const void* b_bf16, const void* x_bf16,
+                                 const float* hidden, int64_t M, int64_t N, int64_t K, int64_t R,
+                                 int64_t num_adapters, const int32_t* adapter_ids, const float* scales,
+                                 const void* base_bf16, const void* d_x_bf16, const float* d_a, const float* d_b,
+                                 const void* workspace, size_t workspace_bytes) {
+  return check_adapter_backward(false, d_out_bf16, a_bf16, b_bf16, x_bf16, hidden, M, N, K, R, num_adapters,
+                                adapter_ids, scales, base_bf16, d_x_bf16, d_a, d_b, workspace, workspace_bytes);
+}
+
+int q4_validate_adapter_backward_f32(const void* d_out_f32, const void* a_f32, const void* b_f32, const void* x_f32,
+                                     const float* hidden, int64_t M, int64_t N, int64_t K, int64_t R,
+                                     int64_t num_adapters, const int32_t* adapter_ids, const float* scales,
+                                     const void* base_f32, const void* d_x_f32, const float* d_a, const float* d_b,
+                                     const void* workspace, size_t workspace_bytes) {
+  return check_adapter_backward(true, d_out_f32, a_f32, b_f32, x_f32, hidden, M, N, K, R, num_adapters, adapter_ids,
+                                scales, base_f32, d_x_f32, d_a, d_b, workspace, workspace_bytes);
 }
 
 size_t q4_route_workspace_bytes(int64_t M, int64_t E) {

@@ -65,3 +65,62 @@ def test_linear_backward_workspace():
     assert q4.linear_backward_workspace_bytes(1, 1, 8) % 256 == 0
     for M, N, K in ((0, 8, 8), (1, 0, 8), (1, 8, 0), (1, 8, 12), (65536, 8, 8), (1, 1 << 40, 4096), (1, 8, 65544)):
         assert q4.linear_backward_workspace_bytes(M, N, K) == 0
+
+
+def _adapter(xdtype="bf16", **kw):
+    a = dict(a=W, b=B, x=X, M=4, N=4096, K=4096, R=16, num_adapters=3, out=OUT, workspace=WS, workspace_bytes=1 << 26)
+    a.update(kw)
+    return q4.validate_adapter(xdtype=xdtype, **a), q4.last_error()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(M=65535, workspace_bytes=1 << 32), dict(N=1), dict(N=1 << 20), dict(K=8), dict(K=65536),
+                                dict(R=8), dict(R=256), dict(num_adapters=65535), dict(adapter_ids=IDS, scales=S, hidden=S),
+                                dict(base=OUT), dict(base=S + 2, out=OUT + 2), dict(xdtype="f32", base=S + 4, out=OUT + 4)])
+def test_adapter_accepts(kw):
+    assert _adapter(**kw) == (0, "")
+
+
+SIZE_FAULTS = [(dict(M=0), INVALID), (dict(M=-3), INVALID), (dict(N=0), INVALID), (dict(K=0), INVALID), (dict(K=12), INVALID),
+               (dict(R=0), INVALID), (dict(R=4), INVALID), (dict(R=-8), INVALID), (dict(num_adapters=0), INVALID),
+               (dict(M=65536), UNSUPPORTED), (dict(N=(1 << 20) + 1), UNSUPPORTED), (dict(K=65544), UNSUPPORTED),
+               (dict(R=264), UNSUPPORTED), (dict(num_adapters=65536), UNSUPPORTED), (dict(workspace=None), WORKSPACE),
+               (dict(workspace=WS + 16), ALIGN), (dict(workspace_bytes=0), WORKSPACE), (dict(a=None), INVALID),
+               (dict(b=None), INVALID), (dict(a=W + 8), ALIGN), (dict(b=B + 8), ALIGN), (dict(x=X + 8), ALIGN),
+               (dict(adapter_ids=IDS + 2), ALIGN), (dict(scales=S + 2), ALIGN), (dict(hidden=S + 8), ALIGN)]
+
+
+@pytest.mark.parametrize("kw,status", SIZE_FAULTS + [
+    (dict(x=None), INVALID), (dict(out=None), INVALID), (dict(out=OUT + 1), ALIGN), (dict(base=S + 1), ALIGN),
+    (dict(out=OUT + 2, xdtype="f32"), ALIGN), (dict(base=S + 2, xdtype="f32"), ALIGN)])
+def test_adapter_refuses(kw, status):
+    got, message = _adapter(**kw)
+    assert got == status and message
+
+
+def _adapter_back(xdtype="bf16", **kw):
+    a = dict(d_out=X, a=W, b=B, M=4, N=4096, K=4096, R=16, num_adapters=3, workspace=WS, workspace_bytes=1 << 26, x=X,
+             hidden=S, d_x=OUT, d_a=OUT, d_b=OUT)
+    a.update(kw)
+    return q4.validate_adapter_backward(xdtype=xdtype, **a), q4.last_error()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(d_x=None), dict(d_a=None, x=None), dict(d_b=None, hidden=None), dict(base=OUT),
+                                dict(d_out=X + 2), dict(d_x=None, d_a=None, x=None), dict(xdtype="f32", d_out=X + 4)])
+def test_adapter_backward_accepts(kw):
+    assert _adapter_back(**kw) == (0, "")
+
+
+@pytest.mark.parametrize("kw,status", SIZE_FAULTS + [
+    (dict(d_out=None), INVALID), (dict(d_x=None, d_a=None, d_b=None), INVALID), (dict(x=None), INVALID),
+    (dict(hidden=None), INVALID), (dict(d_x=None, base=OUT), INVALID), (dict(d_out=X + 1), ALIGN), (dict(d_x=OUT + 8), ALIGN),
+    (dict(d_a=OUT + 8), ALIGN), (dict(d_b=OUT + 8), ALIGN), (dict(base=OUT + 8), ALIGN),
+    (dict(d_out=X + 2, xdtype="f32"), ALIGN)])
+def test_adapter_backward_refuses(kw, status):
+    got, message = _adapter_back(**kw)
+    assert got == status and message
+
+
+def test_adapter_workspace():
+    assert q4.adapter_workspace_bytes(1, 1, 8, 8, 1) % 256 == 0
+    for sizes in ((0, 1, 8, 8, 1), (1, 0, 8, 8, 1), (1, 1, 4, 8, 1), (1, 1, 8, 12, 1), (1, 1, 8, 8, 0), (65536, 1, 8, 8, 1)):
+        assert q4.adapter_workspace_bytes(*sizes) == 0

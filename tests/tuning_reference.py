@@ -67,3 +67,33 @@ def linear_backward(weights, scales, biases, group, d_out, N, K):
     W = dense_weights(weights, scales, biases, group, N, K)
     d = np.asarray(d_out, np.float64)
     return d @ W, np.abs(d) @ np.abs(W)
+
+
+def adapter(a, b, x, ids, scales, base):
+    """(out [M, N], its magnitude, hidden [M, R], its magnitude); scales and base are arrays."""
+    M, (n, N, R) = x.shape[0], b.shape
+    out, mag = np.array(base, np.float64), np.abs(np.array(base, np.float64))
+    h, hm = np.zeros((M, R)), np.zeros((M, R))
+    for t in range(M):
+        i = ids[t]
+        if 0 <= i < n:
+            h[t], hm[t] = a[i] @ x[t], np.abs(a[i]) @ np.abs(x[t])
+            out[t] += scales[i] * (b[i] @ h[t])
+            mag[t] += abs(scales[i]) * (np.abs(b[i]) @ hm[t])
+    return out, mag, h, hm
+
+
+def adapter_backward(d_out, a, b, x, hidden, ids, scales, base):
+    """((d_x, d_a, d_b), their magnitudes)."""
+    n, N, R = b.shape
+    d_x, mx = np.array(base, np.float64), np.abs(np.array(base, np.float64))
+    d_a, ma, d_b, mb = np.zeros(a.shape), np.zeros(a.shape), np.zeros(b.shape), np.zeros(b.shape)
+    for i in range(n):
+        t = np.flatnonzero(np.asarray(ids) == i)
+        d, s = d_out[t], scales[i]
+        g, gm = s * (d @ b[i]), abs(s) * (np.abs(d) @ np.abs(b[i]))
+        d_x[t] += g @ a[i]
+        mx[t] += gm @ np.abs(a[i])
+        d_a[i], ma[i] = g.T @ x[t], gm.T @ np.abs(x[t])
+        d_b[i], mb[i] = s * (d.T @ hidden[t]), abs(s) * (np.abs(d).T @ np.abs(hidden[t]))
+    return (d_x, d_a, d_b), (mx, ma, mb)
