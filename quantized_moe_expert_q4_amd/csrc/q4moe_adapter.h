@@ -1,0 +1,82 @@
+// Shared by the kernels of the low-rank adapters (q4moe_adapter.hip: rows,
+// q4moe_adapter_grad.hip: the gradients of the adapters' matrices).
+#pragma once
+#include "q4moe_device.h"
+#include "q4moe_layer.h"
+#include "q4moe_rows.h"
+
+namespace q4 {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// An element as a float (bf16 is held in a uint16_t), and back.
+template <class T>
+__device__ __forceinline__ float value(T v) {
+  if constexpr (sizeof(T) == 2) return bf16_val(v);
+  else return v;
+}
+template <class T>
+__device__ __forceinline__ T rounded(float v) {
+  if constexpr (sizeof(T) == 2) return __builtin_bit_cast(uint16_t, (__bf16)v);
+  else return v;
+}
+
+__device__ __forceinline__ v4f multiply_bf16(const v4u a, const v4u b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// Eight rows of eight 16-bit values as their eight columns.
+__device__ __forceinline__ void turn(const v4u (&row)[8], v4u (&column)[8]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      column[2 * d][i] = perm(row[2 * i + 1][d], row[2 * i][d], 0x05040100u);
+      column[2 * d + 1][i] = perm(row[2 * i + 1][d], row[2 * i][d], 0x07060302u);
+    }
+}
+
+// Eight floats as PARTS bf16 numbers of eight bits each, highest first (24 bits: all of a float).
+template <int PARTS>
+__device__ __forceinline__ void split(const float (&v)[8], v4u (&part)[PARTS]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a = __float_as_uint(v[2 * i]), b = __float_as_uint(v[2 * i + 1]);
+#pragma unroll
+    for (int d = 0; d < PARTS; ++d) {
+      part[d][i] = perm(b, a, 0x07060302u);
+      a = __float_as_uint(__uint_as_float(a) - __uint_as_float(a & 0xFFFF0000u));
+      b = __float_as_uint(__uint_as_float(b) - __uint_as_float(b & 0xFFFF0000u));
+    }
+  }
+}
+
+// Row's adapter, -1 for an id that names none.
+__device__ __forceinline__ int adapter_of(const int32_t* ids, int row, int n) {
+  const int id = ids ? ids[row] : 0;
+  return (uint32_t)id < (uint32_t)n ? id : -1;
+}
+
+// The gradients of the matrices.  `order` are the rows that have an adapter,
+// by adapter and then in their own order, `offsets` [n + 1] where each adapter's
+// begin; without ids neither is used.
+struct AdapterGradParams {
+  const void* x;          // [M][K]
+  const void* d_out;      // [M][N]
+  const float* g;         // [M][R]
+  const float* hidden;    // [M][R]
+  const int32_t* ids;
+  const float* scales;
+  float* d_a;             // or nullptr
+  float* d_b;             // or nullptr
+  int32_t* order;
+  int32_t* offsets;
+  float* parts;           // sums of adapters whose rows several work-groups share
+  int M, N, K, R, n, xf32;
+};
+
+size_t adapter_grad_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t n);
+hipError_t launch_adapter_grad(const AdapterGradParams& p, hipStream_t stream);
+
+}  // namespace q4

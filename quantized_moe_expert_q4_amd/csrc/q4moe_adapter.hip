@@ -8,47 +8,27 @@
 // serve both directions: "shrink" takes the long rows to R sums, "expand" takes
 // R values to long rows; the adapter's matrix runs along the sum or across it
 // (ACROSS).
-#include "q4moe_device.h"
-#include "q4moe_layer.h"
+#include "q4moe_adapter.h"
 
 namespace q4 {
 
 namespace {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
-
 constexpr int kThreads = 256;
 constexpr int kWindow = 256;         // rows whose adapters a work-group looks at
 constexpr int kTile = 16;            // rows of a work-group
 constexpr int kSlice = 256;          // columns of an expanding work-group
-constexpr int kGradSlice = 64;       // columns of a work-group of the matrices' gradients
 constexpr int kMaxSplits = 16;       // parts of a long sum
 constexpr int kFill = 512;           // work-groups that fill the device: no more parts than give so many
 
+// A chunk's values as floats.
 template <class T>
-__device__ __forceinline__ float value(T v) {
-  if constexpr (sizeof(T) == 2) return bf16_val(v);
-  else return v;
-}
-template <class T>
-__device__ __forceinline__ T rounded(float v) {
-  if constexpr (sizeof(T) == 2) return bf16_rne(v);
-  else return v;
-}
-
-// 16 bytes of a row from element c on as floats, zeros past its C elements.
-template <class T>
-__device__ __forceinline__ void load_values(const T* row, int c, int C, float (&v)[16 / sizeof(T)]) {
-  constexpr int kVec = 16 / sizeof(T);
-  T e[kVec];
-  if (c + kVec <= C) {
-    __builtin_memcpy(e, row + c, 16);
-  } else {
+__device__ __forceinline__ void values(const v4u chunk, float (&v)[16 / sizeof(T)]) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) e[i] = c + i < C ? row[c + i] : (T)0;
+  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) {
+    if constexpr (sizeof(T) == 2) v[i] = __uint_as_float(i & 1 ? chunk[i / 2] & 0xFFFF0000u : chunk[i / 2] << 16);
+    else v[i] = __uint_as_float(chunk[i]);
   }
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) v[i] = value<T>(e[i]);
 }
 
 // The rows of one work-group: `count` of them, all of `adapter` (-1: none).
@@ -56,12 +36,6 @@ struct Rows {
   int row[kTile];
   int adapter, count;
 };
-
-// Row's adapter, -1 for an id that names none.
-__device__ __forceinline__ int adapter_of(const int32_t* ids, int row, int n) {
-  const int id = ids ? ids[row] : 0;
-  return (uint32_t)id < (uint32_t)n ? id : -1;
-}
 
 // Tile `index` of the window's rows: the rows of each adapter, in their order,
 // in tiles of 16, adapters by their first row.  False where there is none.
@@ -131,13 +105,15 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(ShrinkParams p) {
   v4f acc[NR] = {};
   if (adapter >= 0) {
     const T* const w = static_cast<const T*>(p.w) + (size_t)adapter * p.R * p.C;
-    const T* const x = static_cast<const T*>(p.x) + (size_t)s_rows.row[min(l, count - 1)] * p.C;
+    const RowMatrix<T> along(w, p.R, p.C);
+    const RowMatrix<T> x(p.x, p.M, p.C);
+    const int row = s_rows.row[min(l, count - 1)];
     const int steps = (p.C + kStep - 1) / kStep;
     const int begin = steps * (int)blockIdx.z / p.splits, end = steps * ((int)blockIdx.z + 1) / p.splits;
     for (int step = begin + wave; step < end; step += 4) {
       const int c = step * kStep + kVec * g;
       float xv[kVec];
-      load_values<T>(x, c, p.C, xv);
+      values<T>(x.chunk(row, c), xv);
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
         const int r = 16 * j + l;
@@ -147,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(ShrinkParams p) {
 #pragma unroll
             for (int i = 0; i < kVec; ++i) wv[i] = c + i < p.C ? value<T>(w[(size_t)(c + i) * p.R + r]) : 0.0f;
           } else {
-            load_values<T>(w + (size_t)r * p.C, c, p.C, wv);
+            values<T>(along.chunk(r, c), wv);
           }
         }
 #pragma unroll
@@ -175,7 +151,7 @@ struct ExpandParams {
   const float* scales;    // per adapter, or nullptr (1)
   const void* base;       // [M][O] or nullptr
   void* out;              // [M][O]
-  float* hidden;          // [M][R] or nullptr: the sum of the parts
+  float* hidden;          // [M][R] or nullptr: the sum of the parts (ACROSS: scaled)
   int M, O, R, n, splits;
 };
 
@@ -194,11 +170,13 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(ExpandParams p) {
     if (row < count && r < p.R) {
       const size_t at = (size_t)s_rows.row[row] * p.R + r;
       for (int k = 0; k < p.splits; ++k) h += p.partial[(size_t)k * p.M * p.R + at];
-      if (p.hidden && blockIdx.x == 0) p.hidden[at] = h;
+      if (!ACROSS && p.hidden && blockIdx.x == 0) p.hidden[at] = h;
       h *= scale;
+      if (ACROSS && p.hidden && blockIdx.x == 0) p.hidden[at] = h;
     }
     s_h[row][r] = h;
   }
+  if (!p.out) return;
   __syncthreads();
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
   const T* const w = static_cast<const T*>(p.w) + (size_t)max(adapter, 0) * p.R * p.O;
@@ -215,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(ExpandParams p) {
 #pragma unroll
           for (int i = 0; i < kVec; ++i) wv[i] = r + i < p.R ? value<T>(w[(size_t)(r + i) * p.O + o]) : 0.0f;
         } else {
-          load_values<T>(w + (size_t)o * p.R, r, p.R, wv);
+          values<T>(RowMatrix<T>(w, p.O, p.R).chunk(o, r), wv);
         }
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
@@ -231,67 +209,6 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(ExpandParams p) {
         const float b = p.base ? value<T>(static_cast<const T*>(p.base)[at + o]) : 0.0f;
         static_cast<T*>(p.out)[at + o] = rounded<T>(b + acc[i]);
       }
-    }
-  }
-}
-
-struct GradParams {
-  const void* y;          // [M][O]: x, or d_out
-  const float* h;         // [splits][M][R]: the parts of g, or hidden
-  const int32_t* ids;
-  const float* scales;
-  float* grad;            // per adapter [O][R], ACROSS: [R][O]
-  int M, O, R, n, splits;
-};
-
-// grad[o][r] = scale * sum over the adapter's rows of y[row][o] h[row][r].
-template <class T, int NR, bool ACROSS>
-__global__ __launch_bounds__(kThreads) void grad_kernel(GradParams p) {
-  __shared__ int s_list[kWindow + 4], s_count[kThreads / 64];
-  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
-  const int adapter = (int)blockIdx.y;
-  const float scale = p.scales ? p.scales[adapter] : 1.0f;
-  const int o0 = (int)blockIdx.x * kGradSlice + 16 * wave, o = min(o0 + l, p.O - 1);
-  v4f acc[NR] = {};
-  for (int base = 0; base < p.M; base += kWindow) {
-    const int row = base + (int)threadIdx.x;
-    const bool mine = row < p.M && adapter_of(p.ids, row, p.n) == adapter;
-    const uint64_t votes = __ballot(mine);
-    if (lane == 0) s_count[wave] = __popcll(votes);
-    __syncthreads();
-    int at = __popcll(votes & ((1ull << lane) - 1)), count = 0;
-    for (int k = 0; k < kThreads / 64; ++k) {
-      at += k < wave ? s_count[k] : 0;
-      count += s_count[k];
-    }
-    if (mine) s_list[at] = row;
-    if (threadIdx.x < 4) s_list[count + threadIdx.x] = -1;      // count + 4 <= kWindow + 4
-    __syncthreads();
-    for (int i = 0; i < count; i += 4) {
-      const int t = s_list[i + g];
-      const float y = t >= 0 ? value<T>(static_cast<const T*>(p.y)[(size_t)t * p.O + o]) : 0.0f;
-#pragma unroll
-      for (int j = 0; j < NR; ++j) {
-        const int r = 16 * j + l;
-        float h = 0.0f;
-        if (t >= 0 && r < p.R)
-          for (int k = 0; k < p.splits; ++k) h += p.h[((size_t)k * p.M + t) * p.R + r];
-        acc[j] = ACROSS ? __builtin_amdgcn_mfma_f32_16x16x4f32(y, h, acc[j], 0, 0, 0)
-                        : __builtin_amdgcn_mfma_f32_16x16x4f32(h, y, acc[j], 0, 0, 0);
-      }
-    }
-    __syncthreads();
-  }
-  float* const grad = p.grad + (size_t)adapter * p.O * p.R;
-#pragma unroll
-  for (int j = 0; j < NR; ++j) {
-    const v4f v = acc[j] * scale;
-    if constexpr (ACROSS) {
-      const int r = 16 * j + l, k = o0 + 4 * g;
-      if (r < p.R && k < p.O) *reinterpret_cast<v4f*>(grad + (size_t)r * p.O + k) = v;
-    } else {
-      const int r = 16 * j + 4 * g;
-      if (o0 + l < p.O && r < p.R) *reinterpret_cast<v4f*>(grad + (size_t)(o0 + l) * p.R + r) = v;
     }
   }
 }
@@ -336,23 +253,18 @@ hipError_t expand(ExpandParams p, bool f32, bool across, hipStream_t stream) {
   return launch(kernels[f32][across][rank_index(p.R)], p, grid, stream);
 }
 
-hipError_t grad(GradParams p, bool f32, bool across, hipStream_t stream) {
-  static const void* const kernels[2][2][5] = Q4_ADAPTER_KERNELS(grad_kernel);
-  const dim3 grid((unsigned)((p.O + kGradSlice - 1) / kGradSlice), (unsigned)p.n);
-  return launch(kernels[f32][across][rank_index(p.R)], p, grid, stream);
-}
-
 }  // namespace
 
 // The parts of the hidden sums: M rows, or while there are several parts at
 // most kFill tiles in all.
-size_t adapter_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t n) {
-  (void)N;
-  (void)K;
-  (void)n;
+size_t hidden_bytes(int64_t M, int64_t R) {
   const int64_t several = M * kMaxSplits < kFill * kTile ? M * kMaxSplits : kFill * kTile;
   const size_t rows = (size_t)(M > several ? M : several);
   return (rows * (size_t)R * 4 + 255) / 256 * 256;
+}
+
+size_t adapter_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t n) {
+  return hidden_bytes(M, R) + (size_t)M * R * 4 / 256 * 256 + 256 + adapter_grad_workspace(M, N, K, R, n);
 }
 
 hipError_t launch_adapter(const AdapterParams& p, hipStream_t stream) {
@@ -365,15 +277,34 @@ hipError_t launch_adapter(const AdapterParams& p, hipStream_t stream) {
 
 hipError_t launch_adapter_backward(const AdapterBackwardParams& p, hipStream_t stream) {
   const int splits = sum_splits(p.M, p.N);
+  float* const g = p.partial + hidden_bytes(p.M, p.R) / 4;
+  float* const rest = g + (size_t)p.M * p.R / 64 * 64 + 64;
   hipError_t e = hipSuccess;
-  if (p.d_x || p.d_a) e = shrink({p.d_out, p.b, p.ids, p.partial, p.M, p.N, p.R, p.n, splits}, p.xf32, true, stream);
-  if (e == hipSuccess && p.d_x)
-    e = expand({p.partial, p.a, p.ids, p.scales, p.base, p.d_x, nullptr, p.M, p.K, p.R, p.n, splits}, p.xf32, true, stream);
-  if (e == hipSuccess && p.d_a)
-    e = grad({p.x, p.partial, p.ids, p.scales, p.d_a, p.M, p.K, p.R, p.n, splits}, p.xf32, true, stream);
-  if (e == hipSuccess && p.d_b)
-    e = grad({p.d_out, p.hidden, p.ids, p.scales, p.d_b, p.M, p.N, p.R, p.n, 1}, p.xf32, false, stream);
-  return e;
+  if (p.d_x || p.d_a) {
+    e = shrink({p.d_out, p.b, p.ids, p.partial, p.M, p.N, p.R, p.n, splits}, p.xf32, true, stream);
+    if (e == hipSuccess)
+      e = expand({p.partial, p.a, p.ids, p.scales, p.base, p.d_x, g, p.M, p.K, p.R, p.n, splits}, p.xf32, true, stream);
+  }
+  if (e != hipSuccess || (!p.d_a && !p.d_b)) return e;
+  AdapterGradParams q{};
+  q.x = p.x;
+  q.d_out = p.d_out;
+  q.g = g;
+  q.hidden = p.hidden;
+  q.ids = p.ids;
+  q.scales = p.scales;
+  q.d_a = p.d_a;
+  q.d_b = p.d_b;
+  q.order = reinterpret_cast<int32_t*>(rest);
+  q.offsets = q.order + ((size_t)p.M + 63) / 64 * 64;
+  q.parts = reinterpret_cast<float*>(q.offsets + ((size_t)p.n + 64) / 64 * 64);
+  q.M = p.M;
+  q.N = p.N;
+  q.K = p.K;
+  q.R = p.R;
+  q.n = p.n;
+  q.xf32 = p.xf32;
+  return launch_adapter_grad(q, stream);
 }
 
 }  // namespace q4

@@ -1,0 +1,324 @@
+// Gradients of the adapters' matrices,
+//   d_a[r][k] = sum_t g[t][r] x[t][k],   d_b[n][r] = s sum_t d_out[t][n] hidden[t][r],
+// over the rows t of each adapter.
+//
+// The rows are sorted by adapter first (order_kernel, without atomics: the same
+// order on every run) and cut into chunks of `rows`.  A work-group takes a slice
+// of the long dimension and a chunk: its eight waves each take 32 rows at a time,
+// read 16 bytes of each (whole runs of 256 bytes), turn them in registers into
+// matrix operands along the rows, and multiply them with the short vectors, which
+// enter as three bf16 parts, so that nothing of their 24 bits is lost.  An
+// adapter whose rows end within one chunk is written at once, the others' parts
+// are joined in order by a second launch, which also writes the zeros of the
+// adapters without rows.
+#include "q4moe_adapter.h"
+
+namespace q4 {
+
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kOrderWaves = 4;
+constexpr int kRanks = 32;           // ranks of a wave at most: more sums would not fit its registers
+constexpr int kFill = 512;           // work-groups that fill the device: no more chunks than give so many
+constexpr int kLeastRows = 256;      // rows that a chunk has at least: 32 of each wave
+
+// Columns of a work-group's slice.
+template <class T>
+constexpr int kColumns = 256 / (int)sizeof(T);
+
+// A wave for each adapter: where its rows begin among the sorted ones, and the rows.
+__global__ __launch_bounds__(64 * kOrderWaves) void order_kernel(const int32_t* ids, int M, int n, int32_t* order,
+                                                                 int32_t* offsets) {
+  const int lane = threadIdx.x & 63;
+  const int adapter = (int)blockIdx.x * kOrderWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if (adapter >= n) return;
+  constexpr int kAhead = 8;
+  int start = 0, count = 0;
+  for (int t0 = 0; t0 < M; t0 += 64 * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int t = t0 + 64 * k + lane;
+      id[k] = ids[t < M ? t : M - 1];
+      id[k] = t < M ? id[k] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      start += __popcll(__ballot(id[k] >= 0 && id[k] < adapter));
+      count += __popcll(__ballot(id[k] == adapter));
+    }
+  }
+  if (lane == 0) {
+    offsets[adapter] = start;
+    if (adapter == n - 1) offsets[n] = start + count;
+  }
+  if (!count) return;
+  int at = start;
+  for (int t0 = 0; t0 < M; t0 += 64 * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int t = t0 + 64 * k + lane;
+      id[k] = ids[t < M ? t : M - 1];
+      id[k] = t < M ? id[k] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const uint64_t votes = __ballot(id[k] == adapter);
+      if (id[k] == adapter) order[at + __popcll(votes & ((1ull << lane) - 1))] = t0 + 64 * k + lane;
+      at += __popcll(votes);
+    }
+  }
+}
+
+// One of the two gradients: y's columns against h's ranks.
+struct Grad {
+  const void* y;          // [M][O]
+  const float* h;         // [M][R]
+  float* out;             // per adapter [O][R], or [R][O] for d_a
+  float* parts;           // [2 chunks][O][R] or [R][O]: of the adapter that began before the chunk, of one that goes on
+  const float* scales;    // or nullptr
+  int O, slices, rows, chunks;
+};
+
+struct GradLaunch {
+  Grad a, b;
+  const int32_t* ids;
+  const int32_t* order;
+  const int32_t* offsets;
+  int M, R, n;
+  int shift;              // 1 << shift waves share the ranks, the others the rows
+};
+
+// The 32 rows from `at` on as a lane takes them: of bf16 the eight rows of its
+// lane group (a matrix operation takes 32 rows), of float one of each four (it
+// takes 4).
+template <class T>
+__device__ __forceinline__ int row_of(int lane_group, int i) {
+  return sizeof(T) == 2 ? 8 * lane_group + i : 4 * i + lane_group;
+}
+
+// NR: tiles of 16 ranks of a wave.
+template <class T, int NR, bool IS_A>
+__device__ __forceinline__ void grad_slice(const GradLaunch& p, const Grad& q, int slice, int chunk,
+                                           v4f (*s_sum)[NR][64]) {
+  constexpr int kVec = 16 / sizeof(T);           // columns of a lane, one in each of as many tiles of 16
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int rank_waves = 1 << p.shift, rank0 = 16 * NR * (wave & (rank_waves - 1));
+  const int step = 32 * (kWaves >> p.shift);     // rows of the work-group at a time
+  const int o0 = slice * kColumns<T>, col = o0 + kVec * l;
+  const int total = p.ids ? p.offsets[p.n] : p.M;
+  const int chunk_begin = chunk * q.rows, chunk_end = min(total, chunk_begin + q.rows);
+  const ColumnRuns<T> y(q.y, p.M, q.O);
+  const bool ragged = o0 + kColumns<T> > q.O;    // the slice with the rows' ends
+  int begin = chunk_begin;
+  while (begin < chunk_end) {                    // the adapters of the chunk
+    const int adapter = p.ids ? p.ids[p.order[begin]] : 0;
+    const int whole_end = p.ids ? p.offsets[adapter + 1] : p.M, end = min(chunk_end, whole_end);
+    const bool before = begin == chunk_begin && (p.ids ? p.offsets[adapter] : 0) < chunk_begin;
+    const bool several = before || whole_end > end;
+    v4f acc[kVec][NR] = {};
+    // The next rows are fetched as soon as the registers of these are free: y
+    // once it is turned, h rank tile by rank tile.  Loads are unconditional: past
+    // the adapter's rows the last one is repeated, with h = 0; past the columns
+    // and ranks other values come along, whose results are not stored.
+    v4u rows[8];
+    float h[NR][8];
+    int t[8];
+    auto fetch_rows = [&](int at) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int pos = min(at + row_of<T>(g, i), end - 1);
+        t[i] = p.ids ? p.order[pos] : pos;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rows[i] = y.load(t[i], col);
+      if (ragged) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rows[i] = y.aligned(rows[i], t[i], col);
+      }
+    };
+    auto fetch_ranks = [&](int at, int j) {
+      const int r = min(rank0 + 16 * j + l, p.R - 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = q.h[(size_t)t[i] * p.R + r];
+      if (at + 32 > end) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = at + row_of<T>(g, i) < end ? h[j][i] : 0.0f;
+      }
+    };
+    int at = rank0 < p.R ? begin + 32 * (wave >> p.shift) : end;
+    if (at < end) {
+      fetch_rows(at);
+#pragma unroll
+      for (int j = 0; j < NR; ++j) fetch_ranks(at, j);
+    }
+    while (at < end) {
+      const int next = at + step;
+      v4u column[8];
+      if constexpr (sizeof(T) == 2) {
+        turn(rows, column);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) column[i] = rows[i];
+      }
+      if (next < end) fetch_rows(next);
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          v4u part[3];
+          split<3>(h[j], part);
+          if (next < end) fetch_ranks(next, j);
+#pragma unroll
+          for (int d = 0; d < 3; ++d)
+#pragma unroll
+            for (int c = 0; c < kVec; ++c)
+              acc[c][j] = IS_A ? multiply_bf16(column[c], part[d], acc[c][j]) : multiply_bf16(part[d], column[c], acc[c][j]);
+        } else {
+          float now[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) now[i] = h[j][i];
+          if (next < end) fetch_ranks(next, j);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+              const float v = __uint_as_float(column[i][c]);
+              acc[c][j] = IS_A ? __builtin_amdgcn_mfma_f32_16x16x4f32(v, now[i], acc[c][j], 0, 0, 0)
+                               : __builtin_amdgcn_mfma_f32_16x16x4f32(now[i], v, acc[c][j], 0, 0, 0);
+            }
+        }
+      }
+      at = next;
+    }
+    // the waves' sums, tile by tile
+    const float scale = q.scales ? q.scales[adapter] : 1.0f;
+    float* const out = several ? q.parts + (size_t)(2 * chunk + (begin == chunk_begin ? 0 : 1)) * q.O * p.R
+                               : q.out + (size_t)adapter * q.O * p.R;
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NR; ++j) s_sum[wave][j][lane] = acc[c][j];
+      __syncthreads();
+      for (int i = threadIdx.x; i < (NR * 64) << p.shift; i += kThreads) {
+        const int tile = i >> 6, j = tile % NR, first = tile / NR, from = i & 63, fl = from & 15, fg = from >> 4;
+        v4f v = s_sum[first][j][from];
+        for (int w = first + rank_waves; w < kWaves; w += rank_waves) v += s_sum[w][j][from];
+        v *= scale;
+        if constexpr (IS_A) {
+          const int r = 16 * tile + fl;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int o = o0 + kVec * (4 * fg + e) + c;
+            if (r < p.R && o < q.O) out[(size_t)r * q.O + o] = v[e];
+          }
+        } else {
+          const int r = 16 * tile + 4 * fg, o = o0 + kVec * fl + c;
+          if (r < p.R && o < q.O) *reinterpret_cast<v4f*>(out + (size_t)o * p.R + r) = v;
+        }
+      }
+    }
+    begin = end;
+  }
+}
+
+template <class T, int NR>
+__global__ __launch_bounds__(kThreads, 2) void grad_kernel(GradLaunch p) {
+  __shared__ v4f s_sum[kWaves][NR][64];
+  int i = (int)blockIdx.x;
+  if (i < p.a.slices * p.a.chunks) {
+    grad_slice<T, NR, true>(p, p.a, i % p.a.slices, i / p.a.slices, s_sum);
+  } else {
+    i -= p.a.slices * p.a.chunks;
+    grad_slice<T, NR, false>(p, p.b, i % p.b.slices, i / p.b.slices, s_sum);
+  }
+}
+
+// The adapters that the chunks left: those of several chunks, and those without rows.
+__global__ __launch_bounds__(256) void join_kernel(GradLaunch p, Grad q) {
+  const size_t all = (size_t)q.O * p.R / 4, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  for (int adapter = (int)blockIdx.y; adapter < p.n; adapter += (int)gridDim.y) {
+    const int begin = p.ids ? p.offsets[adapter] : adapter ? p.M : 0, end = p.ids ? p.offsets[adapter + 1] : p.M;
+    const int first = begin / q.rows, last = (end - 1) / q.rows;
+    if ((begin < end && first == last) || i >= all) continue;
+    v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (begin < end)
+      for (int c = first; c <= last; ++c) {
+        const int slot = 2 * c + (c == first && begin != c * q.rows ? 1 : 0);
+        sum += reinterpret_cast<const v4f*>(q.parts)[(size_t)slot * all + i];
+      }
+    reinterpret_cast<v4f*>(q.out)[(size_t)adapter * all + i] = sum;
+  }
+}
+
+int chunk_count(int M, int O, int columns) {
+  const int slices = (O + columns - 1) / columns, most = (M + kLeastRows - 1) / kLeastRows;
+  const int c = (kFill + slices - 1) / slices;
+  return c < most ? c : most;
+}
+
+Grad grad_of(const AdapterGradParams& p, const void* y, const float* h, float* out, const float* scales, int O,
+             float* parts) {
+  const int columns = p.xf32 ? kColumns<float> : kColumns<uint16_t>;
+  Grad q{y, h, out, parts, scales, O, out ? (O + columns - 1) / columns : 0, 0, 0};
+  const int chunks = chunk_count(p.M, O, columns);
+  q.rows = ((p.M + chunks - 1) / chunks + 31) / 32 * 32;
+  q.chunks = (p.M + q.rows - 1) / q.rows;
+  return q;
+}
+
+// Bytes of a gradient's parts, two for each chunk: chunk_count(M, O) * O is at
+// most the smaller of ceil(M / kLeastRows) * O and kFill * columns + O.
+size_t part_bytes(int64_t M, int64_t O, int64_t R) {
+  const int64_t by_rows = (M + kLeastRows - 1) / kLeastRows * O, by_fill = kFill * kColumns<uint16_t> + O;
+  return (size_t)(by_rows < by_fill ? by_rows : by_fill) * (size_t)R * 8;
+}
+
+size_t up(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+template <class T>
+const void* pick(int R) {
+  return R <= 16 ? reinterpret_cast<const void*>(&grad_kernel<T, 1>) : reinterpret_cast<const void*>(&grad_kernel<T, 2>);
+}
+
+}  // namespace
+
+// In this order: sorted rows, where the adapters begin, the parts of d_b and of d_a.
+size_t adapter_grad_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t n) {
+  return up((size_t)M * 4) + up((size_t)(n + 1) * 4) + up(part_bytes(M, N, R)) + up(part_bytes(M, K, R));
+}
+
+hipError_t launch_adapter_grad(const AdapterGradParams& p, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (p.ids) {
+    const int32_t* ids = p.ids;
+    int M = p.M, n = p.n;
+    int32_t *order = p.order, *offsets = p.offsets;
+    void* args[] = {&ids, &M, &n, &order, &offsets};
+    e = hipLaunchKernel(reinterpret_cast<const void*>(&order_kernel), dim3((unsigned)((n + kOrderWaves - 1) / kOrderWaves)),
+                        dim3(64 * kOrderWaves), args, 0, stream);
+    if (e != hipSuccess) return e;
+  }
+  float* const parts_a = p.parts + up(part_bytes(p.M, p.N, p.R)) / 4;
+  GradLaunch q{grad_of(p, p.x, p.g, p.d_a, nullptr, p.K, parts_a), grad_of(p, p.d_out, p.hidden, p.d_b, p.scales, p.N, p.parts),
+               p.ids, p.order, p.offsets, p.M, p.R, p.n, 0};
+  while ((kRanks << q.shift) < p.R) ++q.shift;
+  void* args[] = {&q};
+  const unsigned blocks = (unsigned)(q.a.slices * q.a.chunks + q.b.slices * q.b.chunks);
+  e = hipLaunchKernel(p.xf32 ? pick<float>(p.R) : pick<uint16_t>(p.R), dim3(blocks),
+                      dim3(kThreads), args, 0, stream);
+  for (Grad* one : {&q.a, &q.b}) {
+    if (e != hipSuccess || !one->out || (!p.ids && p.n == 1 && one->chunks == 1)) continue;
+    void* join_args[] = {&q, one};
+    const size_t all = (size_t)one->O * p.R / 4;
+    e = hipLaunchKernel(reinterpret_cast<const void*>(&join_kernel), dim3((unsigned)((all + 255) / 256), (unsigned)p.n),
+                        dim3(256), join_args, 0, stream);
+  }
+  return e;
+}
+
+}  // namespace q4

@@ -10,6 +10,7 @@
 // is one 16-byte read.
 #include "q4moe_device.h"
 #include "q4moe_layer.h"
+#include "q4moe_rows.h"
 
 namespace q4 {
 
@@ -26,23 +27,6 @@ constexpr int kCols = 128;           // columns k of a work-group
 constexpr int kChunks = 8;           // 16-byte chunks of a tile's row
 constexpr int kMaxSplits = 16;       // parts of n that work-groups share
 constexpr int kFill = 512;           // work-groups that fill the device: no more parts than give so many
-
-// 16 bytes of a row from element n0 on, zeros past its N elements.  Rows may
-// start at any multiple of the element.
-template <class T>
-__device__ __forceinline__ v4u load_chunk(const T* row, int n0, int N) {
-  constexpr int kVec = 16 / sizeof(T);
-  v4u r = {0, 0, 0, 0};
-  if (n0 + kVec <= N) {
-    __builtin_memcpy(&r, row + n0, 16);
-  } else {
-    T e[kVec];
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) e[i] = n0 + i < N ? row[n0 + i] : (T)0;
-    __builtin_memcpy(&r, e, 16);
-  }
-  return r;
-}
 
 // Place of a row's chunk: the eight chunks change places from row to row and
 // from eight rows to the next, so that neither the reads (16 rows of one chunk)
@@ -88,6 +72,8 @@ __global__ __launch_bounds__(kThreads) void linear_back_kernel(LinearBackParams 
   const uint32_t* const w_at = reinterpret_cast<const uint32_t*>(p.w) + (k0 / 8 + (col_in ? kb : 0));
   const int group = (k0 + (col_in ? 8 * kb : 0)) / p.group;
 
+  const RowMatrix<T> d_out(p.d_out, p.M, p.N);
+
   struct Fetched {
     v4u d[kRows];
     uint32_t w[kWords];
@@ -99,7 +85,7 @@ __global__ __launch_bounds__(kThreads) void linear_back_kernel(LinearBackParams 
     for (int i = 0; i < kRows; ++i) {
       const int row = tid / kChunks + 32 * i, m = min(m0 + row, p.M - 1);      // rows past the last one repeat it
       if (BM >= 32 || row < BM)
-        f.d[i] = load_chunk(static_cast<const T*>(p.d_out) + (size_t)m * p.N, n0 + (tid % kChunks) * kVec, p.N);
+        f.d[i] = d_out.chunk(m, n0 + (tid % kChunks) * kVec);
     }
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
