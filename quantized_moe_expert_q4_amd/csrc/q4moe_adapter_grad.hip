@@ -19,7 +19,6 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kOrderWaves = 4;
 constexpr int kRanks = 32;           // ranks of a wave at most: more sums would not fit its registers
 constexpr int kFill = 512;           // work-groups that fill the device: no more chunks than give so many
 constexpr int kLeastRows = 256;      // rows that a chunk has at least: 32 of each wave
@@ -28,49 +27,55 @@ constexpr int kLeastRows = 256;      // rows that a chunk has at least: 32 of ea
 template <class T>
 constexpr int kColumns = 256 / (int)sizeof(T);
 
-// A wave for each adapter: where its rows begin among the sorted ones, and the rows.
-__global__ __launch_bounds__(64 * kOrderWaves) void order_kernel(const int32_t* ids, int M, int n, int32_t* order,
-                                                                 int32_t* offsets) {
-  const int lane = threadIdx.x & 63;
-  const int adapter = (int)blockIdx.x * kOrderWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  if (adapter >= n) return;
+// A work-group for each adapter: where its rows begin among the sorted ones, and
+// the rows.  Each wave takes a run of the rows; it is read twice, first to count.
+__global__ __launch_bounds__(kThreads) void order_kernel(const int32_t* ids, int M, int n, int32_t* order,
+                                                         int32_t* offsets) {
   constexpr int kAhead = 8;
-  int start = 0, count = 0;
-  for (int t0 = 0; t0 < M; t0 += 64 * kAhead) {
-    int id[kAhead];
+  __shared__ int s_below[kWaves], s_mine[kWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int adapter = (int)blockIdx.x;
+  const int steps = (M + 63) / 64, begin = 64 * (steps * wave / kWaves), end = min(M, 64 * (steps * (wave + 1) / kWaves));
+  const auto visit = [&](auto&& see) {
+    for (int t0 = begin; t0 < end; t0 += 64 * kAhead) {
+      int id[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int t = t0 + 64 * k + lane;
-      id[k] = ids[t < M ? t : M - 1];
-      id[k] = t < M ? id[k] : -1;
-    }
+      for (int k = 0; k < kAhead; ++k) id[k] = ids[min(t0 + 64 * k + lane, M - 1)];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      start += __popcll(__ballot(id[k] >= 0 && id[k] < adapter));
-      count += __popcll(__ballot(id[k] == adapter));
+      for (int k = 0; k < kAhead; ++k) {
+        const int t = t0 + 64 * k + lane;
+        see(t, t < end ? id[k] : -1);
+      }
     }
-  }
+  };
+  int below = 0, mine = 0;
+  visit([&](int, int id) {
+    below += __popcll(__ballot(id >= 0 && id < adapter));
+    mine += __popcll(__ballot(id == adapter));
+  });
   if (lane == 0) {
+    s_below[wave] = below;
+    s_mine[wave] = mine;
+  }
+  __syncthreads();
+  int start = 0, at = 0, count = 0;
+  for (int w = 0; w < kWaves; ++w) {
+    start += s_below[w];
+    at += w < wave ? s_mine[w] : 0;
+    count += s_mine[w];
+  }
+  if (threadIdx.x == 0) {
     offsets[adapter] = start;
     if (adapter == n - 1) offsets[n] = start + count;
   }
-  if (!count) return;
-  int at = start;
-  for (int t0 = 0; t0 < M; t0 += 64 * kAhead) {
-    int id[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int t = t0 + 64 * k + lane;
-      id[k] = ids[t < M ? t : M - 1];
-      id[k] = t < M ? id[k] : -1;
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const uint64_t votes = __ballot(id[k] == adapter);
-      if (id[k] == adapter) order[at + __popcll(votes & ((1ull << lane) - 1))] = t0 + 64 * k + lane;
-      at += __popcll(votes);
-    }
-  }
+  if (!mine) return;
+  at += start;
+  visit([&](int t, int id) {
+    const uint64_t votes = __ballot(id == adapter);
+    if (id == adapter) order[at + __popcll(votes & ((1ull << lane) - 1))] = t;
+    at += __popcll(votes);
+  });
 }
 
 // One of the two gradients: y's columns against h's ranks.
@@ -299,8 +304,8 @@ hipError_t launch_adapter_grad(const AdapterGradParams& p, hipStream_t stream) {
     int M = p.M, n = p.n;
     int32_t *order = p.order, *offsets = p.offsets;
     void* args[] = {&ids, &M, &n, &order, &offsets};
-    e = hipLaunchKernel(reinterpret_cast<const void*>(&order_kernel), dim3((unsigned)((n + kOrderWaves - 1) / kOrderWaves)),
-                        dim3(64 * kOrderWaves), args, 0, stream);
+    e = hipLaunchKernel(reinterpret_cast<const void*>(&order_kernel), dim3((unsigned)n),
+                        dim3(kThreads), args, 0, stream);
     if (e != hipSuccess) return e;
   }
   float* const parts_a = p.parts + up(part_bytes(p.M, p.N, p.R)) / 4;
