@@ -9,6 +9,7 @@ namespace q4 {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 // An element as a float (bf16 is held in a uint16_t), and back.
 template <class T>
@@ -26,10 +27,12 @@ __device__ __forceinline__ v4f multiply_bf16(const v4u a, const v4u b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// Eight rows of eight 16-bit values as their eight columns.
-__device__ __forceinline__ void turn(const v4u (&row)[8], v4u (&column)[8]) {
+// Eight rows of eight (four) 16-bit values as their columns.
+template <class ROW, int COLUMNS>
+__device__ __forceinline__ void turn(const ROW (&row)[8], v4u (&column)[COLUMNS]) {
+  static_assert(sizeof(ROW) == 2 * COLUMNS, "a row holds the columns");
 #pragma unroll
-  for (int d = 0; d < 4; ++d)
+  for (int d = 0; d < COLUMNS / 2; ++d)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       column[2 * d][i] = perm(row[2 * i + 1][d], row[2 * i][d], 0x05040100u);

@@ -4,15 +4,16 @@
 //   backward  g = s B^T d, d_x = base + A^T g (and in q4moe_adapter_grad.hip
 //             d_A = sum_t g x^T, d_B = s sum_t d h^T)
 //
-// A work-group takes 16 rows of one adapter, gathered from a window of 256 rows
-// (group_rows), so that rows of one adapter need not stand together.  Both
+// A work-group takes 16 rows of one adapter (of large batches 64, which read the
+// adapter a quarter as often), gathered from a window of 256 rows (group_rows),
+// so that rows of one adapter need not stand together.  Both
 // directions take long rows to R sums ("shrink") and those to long rows
 // ("expand"); the adapter's matrix runs along the sum, or across it (ACROSS, the
 // backward pass).  The R sums of the rows stay in LDS between the two; only
 // where few rows would leave the device idle are there two launches, the first
 // with several work-groups along the long sum.
 //
-// Matrix operations take the adapter as rows and the 16 tokens as columns.  bf16:
+// Matrix operations take the adapter as rows and 16 tokens as columns.  bf16:
 // the values between the products enter the second as two bf16 parts (16 bits).
 #include "q4moe_adapter.h"
 
@@ -23,68 +24,105 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kWindow = 256;         // rows whose adapters a work-group looks at
-constexpr int kTile = 16;            // rows of a work-group
+constexpr int kTile = 16;            // rows of a matrix operation
 constexpr int kMaxSplits = 16;       // parts of a long sum
+constexpr int kLargeBatch = 1024;    // rows from which on a work-group takes 64
 constexpr int kFill = 512;           // work-groups that fill the device: no more parts than give so many
 
-// The rows of one work-group: `count` of them, all of `adapter` (-1: none).
+// The rows of one work-group: `count` of them, all of `adapter` (-1: none);
+// row(i) is the i-th.
 struct Rows {
-  int row[kTile];
+  const int* list;
   int adapter, count;
+  __device__ __forceinline__ int row(int i) const { return list[i]; }
 };
 
 // Tile `index` of the window's rows: the rows of each adapter, in their order,
-// in tiles of 16, adapters by their first row.  False where there is none.
-__device__ __forceinline__ bool group_rows(const int32_t* ids, int M, int n, int window, int index, Rows& out) {
-  __shared__ int s_id[kWindow], s_first[kWindow], s_total[kWindow / 64];
-  const int t = threadIdx.x, row = window * kWindow + t, lane = t & 63, wave = t >> 6;
-  const int rows = min(kWindow, M - window * kWindow);
-  const int id = t < rows ? adapter_of(ids, row, n) : -2;
-  if (t < kWindow) s_id[t] = id;
-  if (t == 0) out.count = 0;
-  __syncthreads();
-  int before = t, same = rows, first = 0;
-  // most windows hold one adapter
-  if (!__syncthreads_and(t >= rows || id == s_id[0])) {
-    before = same = 0;
-    first = t;
-    if (t < rows)
-      for (int j = 0; j < rows; ++j) {
-        const bool eq = s_id[j] == id;
-        same += eq;
-        before += eq && j < t;
-        first = eq && j < first ? j : first;
+// in tiles of ROWS, adapters by their first row; count 0 where there is none.
+// Every wave finds its own copy: four rows a lane, an adapter after the other by
+// votes, without a barrier.
+template <int ROWS>
+__device__ __forceinline__ Rows group_rows(const int32_t* ids, int M, int n, int window, int index) {
+  constexpr int kRuns = kWindow / 64;
+  __shared__ int s_list[kWaves][ROWS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  Rows out{s_list[wave], -1, 0};
+  if (M <= 64) {
+    // every row against every other: the adapters' first tiles by their first
+    // rows, then their second ones, and so on (64 rows of 24 adapters: 0.4 us,
+    // by the loop below 3)
+    const int id = lane < M ? adapter_of(ids, lane, n) : -2;
+    int before = 0, count = 0;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+      const bool eq = __builtin_amdgcn_readlane(id, j) == id;
+      count += eq;
+      before += eq && j < lane;
+    }
+    uint64_t firsts = __ballot(lane < M && before == 0);
+    int skip = 0;                                // rows of the adapter in earlier tiles
+    while (firsts && index >= __popcll(firsts)) {
+      index -= __popcll(firsts);
+      skip += ROWS;
+      firsts = __ballot(lane < M && before == 0 && count > skip);
+    }
+    if (!firsts) return out;
+    const bool chosen = ((firsts >> lane) & 1) && __popcll(firsts & ((1ull << lane) - 1)) == index;
+    const int first = __builtin_ctzll(__ballot(chosen));
+    out.adapter = __builtin_amdgcn_readlane(id, first);
+    out.count = min(ROWS, __builtin_amdgcn_readlane(count, first) - skip);
+    if (id == out.adapter && (uint32_t)(before - skip) < ROWS) s_list[wave][before - skip] = lane;
+    wave_sync();
+    return out;
+  }
+  int id[kRuns];
+  uint64_t left[kRuns], same[kRuns];
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {
+    const int row = window * kWindow + 64 * k + lane;
+    id[k] = adapter_of(ids, min(row, M - 1), n);
+    left[k] = __ballot(row < M);
+  }
+  bool found = false;
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {              // the adapters whose first row is of run k
+    while (!found && left[k]) {
+      const int adapter = __builtin_amdgcn_readlane(id[k], __builtin_ctzll(left[k]));
+      int count = 0;
+#pragma unroll
+      for (int m = 0; m < kRuns; ++m) {
+        same[m] = m < k ? 0 : __ballot(id[m] == adapter) & left[m];
+        count += __popcll(same[m]);
+        left[m] &= ~same[m];
       }
-  }
-  // tiles of the adapters whose first row comes earlier
-  const int tiles = t < rows && before == 0 ? (same + kTile - 1) / kTile : 0;
-  int sum = tiles;
-  for (int d = 1; d < 64; d <<= 1) {
-    const int other = __shfl_up(sum, d);
-    sum += lane >= d ? other : 0;
-  }
-  if (lane == 63 && t < kWindow) s_total[wave] = sum;
-  __syncthreads();
-  int start = sum - tiles;
-  for (int w = 0; w < min(wave, kWindow / 64); ++w) start += s_total[w];
-  if (t < kWindow) s_first[t] = start;
-  __syncthreads();
-  if (t < rows && s_first[first] + before / kTile == index) {
-    out.row[before % kTile] = row;
-    if (before % kTile == 0) {
-      out.adapter = id;
-      out.count = min(kTile, same - before);
+      const int tiles = (count + ROWS - 1) / ROWS;
+      found = index < tiles;
+      if (found) {
+        out.adapter = adapter;
+        out.count = min(ROWS, count - ROWS * index);
+      } else {
+        index -= tiles;
+      }
     }
   }
-  __syncthreads();
-  return out.count > 0;
+  if (!found) return out;
+  int before = -ROWS * index;
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {
+    const int at = before + __popcll(same[k] & ((1ull << lane) - 1));
+    if (((same[k] >> lane) & 1) && (uint32_t)at < ROWS) s_list[wave][at] = window * kWindow + 64 * k + lane;
+    before += __popcll(same[k]);
+  }
+  wave_sync();
+  return out;
 }
 
 // Tiles that a window of M rows can have.
-int window_tiles(int M, int n, bool ids) {
+int window_tiles(int M, int n, bool ids, int tile) {
   const int rows = M < kWindow ? M : kWindow;
   const int kinds = !ids ? 1 : n + 1 < rows ? n + 1 : rows;
-  return (rows + 15 * kinds) / 16;
+  return (rows + (tile - 1) * kinds) / tile;
 }
 
 struct RowsParams {
@@ -117,29 +155,36 @@ template <class T>
 __device__ __forceinline__ int hidden_pitch(int R) {
   return sizeof(T) == 2 ? 2 * R + 16 : 4 * R + 16;
 }
-constexpr int kHiddenBytes = kTile * (4 * 256 + 32);
+template <int NR, int TT>
+constexpr int kHiddenBytes = TT * kTile * (4 * (NR < 8 ? 16 * NR : 256) + 32);
 
-// acc[j]: of the wave's part of the sum, ranks rank0 + 16 j + 4 (lane / 16) .. of row lane % 16.
-template <class T, int NR, bool ACROSS>
-__device__ __forceinline__ void shrink_rows(const RowsParams& p, const T* w, int row, int rank0, int begin, int end,
-                                            uint8_t* s_turn, v4f (&acc)[NR]) {
+// acc[t][j]: of the wave's part of the sum, ranks rank0 + 16 j + 4 (lane / 16) ..
+// of row 16 t + lane % 16; tiles of rows past `tiles` are left out.
+template <class T, int NR, bool ACROSS, int TT>
+__device__ __forceinline__ void shrink_rows(const RowsParams& p, const T* w, const int (&row)[TT], int tiles, int rank0,
+                                            int begin, int end, uint8_t* s_turn, v4f (&acc)[TT][NR]) {
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   if constexpr (!ACROSS && sizeof(T) == 2) {
-    // steps of 64 elements: two operations; 128 bytes of a row are read together.
+    // Steps of 64 elements: two operations; 128 bytes of a row are read together.
     // Past the row's end x is 0 (and what it meets there an element of the same
     // row of the adapter); ranks past R are dropped later.
-    const T* const x = static_cast<const T*>(p.x) + (size_t)row * p.C;
-    constexpr int kBatch = NR >= 4 ? 1 : NR == 2 ? 2 : 4;
+    const T* x[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) x[t] = static_cast<const T*>(p.x) + (size_t)row[t] * p.C;
+    constexpr int kBatch = TT > 1 || NR >= 4 ? 1 : NR == 2 ? 2 : 4;
     for (int s0 = begin + wave * kBatch; s0 < end; s0 += kWaves * kBatch) {
-      v4u xv[kBatch][2], wv[kBatch][NR][2];
+      v4u xv[kBatch][2][TT], wv[kBatch][NR][2];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int c = 64 * (s0 + b) + 16 * g + 8 * h, at = min(c, p.C - 8);
-          xv[b][h] = *reinterpret_cast<const v4u*>(x + at);
-          if (c >= p.C || s0 + b >= end) xv[b][h] = v4u{0, 0, 0, 0};
+          const int c = 64 * (s0 + b) + 32 * h + 8 * g, at = min(c, p.C - 8);
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            xv[b][h][t] = *reinterpret_cast<const v4u*>(x[t] + at);
+            if (c >= p.C || s0 + b >= end) xv[b][h][t] = v4u{0, 0, 0, 0};
+          }
 #pragma unroll
           for (int j = 0; j < NR; ++j)
             wv[b][j][h] = *reinterpret_cast<const v4u*>(w + (size_t)min(rank0 + 16 * j + l, p.R - 1) * p.C + at);
@@ -149,7 +194,11 @@ __device__ __forceinline__ void shrink_rows(const RowsParams& p, const T* w, int
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < NR; ++j) acc[j] = multiply_bf16(wv[b][j][h], xv[b][h], acc[j]);
+          for (int t = 0; t < TT; ++t)
+            if (t < tiles) {
+#pragma unroll
+              for (int j = 0; j < NR; ++j) acc[t][j] = multiply_bf16(wv[b][j][h], xv[b][h][t], acc[t][j]);
+            }
     }
   } else if constexpr (sizeof(T) == 2) {
     // Chunks of kCount elements: a lane reads eight rows of eight ranks, turns
@@ -166,27 +215,44 @@ __device__ __forceinline__ void shrink_rows(const RowsParams& p, const T* w, int
     const RowMatrix<T> x(p.x, p.M, p.C);
     for (int s = begin + wave; s < end; s += kWaves) {
       const int c0 = s * kCount;
-      v4u from[8], column[8], xv[kCount / 32];
+      const bool whole = c0 + kCount <= p.C;
+      const auto load_x = [&](int h, v4u (&xv)[TT]) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const int c = c0 + 32 * h + 8 * g;
+          if (whole) __builtin_memcpy(&xv[t], x.data + (size_t)row[t] * p.C + c, 16);
+          else xv[t] = x.chunk(row[t], c);
+        }
+      };
+      v4u from[8], column[8], xv[2][TT];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         from[i] = *reinterpret_cast<const v4u*>(w + (size_t)min(c0 + 8 * part + i, p.C - 1) * p.R + rank);
-#pragma unroll
-      for (int h = 0; h < kCount / 32; ++h) xv[h] = x.chunk(row, c0 + 32 * h + 8 * g);
+      load_x(0, xv[0]);
       turn(from, column);
       wave_sync();
 #pragma unroll
       for (int i = 0; i < 8; ++i) s_w[place(8 * octet + i, part)] = column[i];
       wave_sync();
 #pragma unroll
-      for (int h = 0; h < kCount / 32; ++h)
+      for (int h = 0; h < kCount / 32; ++h) {
+        if (h + 1 < kCount / 32) load_x(h + 1, xv[(h + 1) & 1]);
 #pragma unroll
-        for (int j = 0; j < NR; ++j) acc[j] = multiply_bf16(s_w[place(16 * j + l, 4 * h + g)], xv[h], acc[j]);
+        for (int j = 0; j < NR; ++j) {
+          const v4u wv = s_w[place(16 * j + l, 4 * h + g)];
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+            if (t < tiles) acc[t][j] = multiply_bf16(wv, xv[h & 1][t], acc[t][j]);
+        }
+      }
     }
   } else {
     const RowMatrix<T> x(p.x, p.M, p.C);
     for (int s = begin + wave; s < end; s += kWaves) {
       const int c = 16 * s + 4 * g;
-      const v4u xv = x.chunk(row, c);
+      v4u xv[TT];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) xv[t] = x.chunk(row[t], c);
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
         const int r = min(rank0 + 16 * j + l, p.R - 1);
@@ -198,8 +264,13 @@ __device__ __forceinline__ void shrink_rows(const RowsParams& p, const T* w, int
           wv = *reinterpret_cast<const v4u*>(w + (size_t)r * p.C + min(c, p.C - 4));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(wv[i]), __uint_as_float(xv[i]), acc[j], 0, 0, 0);
+        for (int t = 0; t < TT; ++t)
+          if (t < tiles) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(wv[i]), __uint_as_float(xv[t][i]), acc[t][j],
+                                                               0, 0, 0);
+          }
       }
     }
   }
@@ -210,7 +281,7 @@ template <class T, int NR, bool ACROSS>
 constexpr int kStep = sizeof(T) == 4 ? 16 : ACROSS ? 256 / NR : 64;
 
 // Keeps four values of the sums (ranks r ..) for the second product.
-template <class T>
+template <class T, int TT>
 __device__ __forceinline__ void keep_hidden(uint8_t* s_hidden, int R, int row, int r, v4f v) {
   if constexpr (sizeof(T) == 2) {
     uint32_t part[2][2];
@@ -224,210 +295,282 @@ __device__ __forceinline__ void keep_hidden(uint8_t* s_hidden, int R, int row, i
     }
 #pragma unroll
     for (int d = 0; d < 2; ++d)
-      __builtin_memcpy(s_hidden + (d * kTile + row) * hidden_pitch<T>(R) + 2 * r, part[d], 8);
+      __builtin_memcpy(s_hidden + (d * TT * kTile + row) * hidden_pitch<T>(R) + 2 * r, part[d], 8);
   } else {
     __builtin_memcpy(s_hidden + row * hidden_pitch<T>(R) + 4 * r, &v, 16);
   }
 }
 
-// Eight consecutive results of a row onto base; O any: rows may start at any element.
-__device__ __forceinline__ void put8(const RowsParams& p, const RowMatrix<uint16_t>& base, int row, int o, const float (&v)[8]) {
-  v4u b = {0, 0, 0, 0};
-  if (p.base) b = base.chunk(row, o);
-  uint16_t r[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    r[i] = rounded<uint16_t>(v[i] + __uint_as_float(i & 1 ? b[i / 2] & 0xFFFF0000u : b[i / 2] << 16));
-  uint16_t* const out = static_cast<uint16_t*>(p.out) + (size_t)row * p.O + o;
-  if (o + 8 <= p.O) {
+// 16 bytes of a row of the results; rows may start at any element.
+template <class T>
+__device__ __forceinline__ void put(const RowsParams& p, int row, int o, const T (&r)[16 / sizeof(T)]) {
+  constexpr int kVec = 16 / sizeof(T);
+  if (row < 0) return;
+  T* const out = static_cast<T*>(p.out) + (size_t)row * p.O + o;
+  if (o + kVec <= p.O) {
     __builtin_memcpy(out, r, 16);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (o + i < p.O) out[i] = r[i];
-  }
-}
-__device__ __forceinline__ void put4(const RowsParams& p, const RowMatrix<float>& base, int row, int o, const v4f v) {
-  v4f r = v;
-  if (p.base) r += __builtin_bit_cast(v4f, base.chunk(row, o));
-  float* const out = static_cast<float*>(p.out) + (size_t)row * p.O + o;
-  if (o + 4 <= p.O) {
-    __builtin_memcpy(out, &r, 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kVec; ++i)
       if (o + i < p.O) out[i] = r[i];
   }
 }
 
-// The work-group's columns [begin, end) of its rows' results.
-template <class T, bool ACROSS>
+constexpr int kUnit = 64;            // columns of a wave's unit of the results
+constexpr int kCols = kUnit / 16;    // operations of a unit
+
+// The results of 16 rows by a unit's columns go through the wave's LDS, so that
+// a load of base and a store cover whole lines of a row: the
+// operation leaves a row's results with four lanes (64-byte pieces, half as fast).
+// Chunks are four floats; bf16 rows take two for a lane's eight columns.
+template <class T>
+struct Bounce {
+  static constexpr int kVec = 16 / (int)sizeof(T);                 // columns of a lane's load
+  static constexpr int kPieces = kUnit / kVec;                     // of a row
+  static constexpr int kRows = 64 / kPieces, kPasses = kTile / kRows;
+  static constexpr int kHalves = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int kBytes = kTile * kUnit * 4;
+  v4f* lds;
+
+  __device__ __forceinline__ v4f& at(int half, int row, int piece) const {
+    return lds[(half * kTile + row) * kPieces + (piece ^ (row & (kPieces - 1)))];
+  }
+};
+
+// The work-group's columns [begin, end) of its rows' results.  A wave takes units
+// of columns: its part of the adapter (blocks of 32 ranks, STEPS of them at a
+// time) stays in registers for all tiles of rows where it is KEPT there.
+template <class T, int STEPS, bool KEPT, bool ACROSS, int TT>
 __device__ __forceinline__ void expand_rows(const RowsParams& p, const T* w, bool live, const Rows& rows,
-                                            const uint8_t* s_hidden, int begin, int end) {
+                                            const uint8_t* s_hidden, uint8_t* s_bounce, int begin, int end) {
+  using B = Bounce<T>;
+  constexpr int kRanks = 32;
+  constexpr int kLoads = sizeof(T) == 2 ? 1 : 2;                   // 16 bytes of a column's (ACROSS: a rank's) 32 ranks
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int row = rows.row[min(l, rows.count - 1)];
-  const bool mine = l < rows.count;
-  const RowMatrix<T> base(p.base, p.M, p.O);
+  const int tiles = (rows.count + kTile - 1) / kTile;
+  const B bounce{reinterpret_cast<v4f*>(s_bounce + wave * B::kBytes)};
+  const int pass_row = lane / B::kPieces, piece = lane % B::kPieces;
+  const RowMatrix<T> base_rows(p.base, p.M, p.O);
   const int pitch = hidden_pitch<T>(p.R);
-  if constexpr (sizeof(T) == 2) {
-    // Eight ranks are a chunk of the sum, of the high parts and then of the low
-    // ones; past those h is 0 (and meets an element of the same row of the adapter).
-    const int chunks = p.R / 8, steps = live ? (2 * chunks + 3) / 4 : 0;
-    const auto part = [&](int s, int& chunk) {
-      const int c = 4 * s + g;
-      const bool low = c >= chunks;
-      chunk = min(low ? c - chunks : c, chunks - 1);
-      v4u h = *reinterpret_cast<const v4u*>(s_hidden + ((low ? kTile : 0) + l) * pitch + 16 * chunk);
-      if (c >= 2 * chunks) h = v4u{0, 0, 0, 0};
-      return h;
+  const int blocks = live ? (p.R + kRanks * STEPS - 1) / (kRanks * STEPS) : 0;
+  for (int o0 = begin + kUnit * wave; o0 < end; o0 += kUnit * kWaves) {
+    const int o = o0 + B::kVec * piece;
+    // the base of all tiles, so that much is on its way
+    v4u base[TT][B::kPasses];
+    const auto row_of = [&](int t, int k) {
+      const int i = kTile * t + B::kRows * k + pass_row;
+      return i < rows.count && o < p.O ? rows.row(i) : -1;
     };
-    if constexpr (ACROSS) {
-      // 128 columns: lane l reads eight of them, which eight tiles share; a lane's
-      // results are the eight columns of octet g + 4 i.
-      const int octet = (l >> 2) + 4 * (l & 3);
-      for (int o0 = begin + 128 * wave; o0 < end; o0 += 128 * kWaves) {
-        v4f acc[8] = {};
-        for (int s = 0; s < steps; ++s) {
-          int chunk;
-          const v4u h = part(s, chunk);
-          v4u from[8], column[8];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int k = 0; k < B::kPasses; ++k) base[t][k] = v4u{0, 0, 0, 0};
+    if (p.base && o0 + kUnit <= p.O) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int k = 0; k < B::kPasses; ++k)
+          if (t < tiles) __builtin_memcpy(&base[t][k], base_rows.data + (size_t)max(row_of(t, k), 0) * p.O + o, 16);
+    } else if (p.base) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int k = 0; k < B::kPasses; ++k)
+          if (t < tiles) base[t][k] = base_rows.chunk(max(row_of(t, k), 0), o);
+    }
+    // bf16: lane group g holds ranks 8 g .. of a block; float: ranks 4 i + g of
+    // it (ACROSS), or 16 i + 4 g .. (two loads).  Past R h is 0, and meets
+    // elements of the same columns.
+    v4u wv[STEPS][sizeof(T) == 2 ? kCols : ACROSS ? 8 : kCols * kLoads];     // ACROSS: of columns 4 l + j
+    const auto load_w = [&](int block) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const int rank0 = kRanks * (STEPS * block + s);
+        if constexpr (sizeof(T) == 2 && ACROSS) {
+          // lane l reads four columns, which four operations share
+          v2u from[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            from[i] = *reinterpret_cast<const v4u*>(w + (size_t)(8 * chunk + i) * p.O + min(o0 + 8 * octet, p.O - 8));
-          turn(from, column);
+            from[i] = *reinterpret_cast<const v2u*>(w + (size_t)min(rank0 + 8 * g + i, p.R - 1) * p.O +
+                                                    min(o0 + 4 * l, p.O - 4));
+          turn(from, wv[s]);
+        } else if constexpr (ACROSS) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = multiply_bf16(column[j], h, acc[j]);
-        }
+          for (int i = 0; i < 8; ++i)
+            wv[s][i] = *reinterpret_cast<const v4u*>(w + (size_t)min(rank0 + 4 * i + g, p.R - 1) * p.O +
+                                                     min(o0 + 4 * l, p.O - 4));
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int o = o0 + 8 * (g + 4 * i);
-          float v[8];
+          for (int j = 0; j < kCols; ++j) {
+            // bf16: pairs of operations whose results give a lane eight neighbours
+            const int at = min(o0 + (sizeof(T) == 2 ? 32 * (j / 2) + 8 * (l >> 2) + 4 * (j % 2) + (l & 3) : 16 * j + l),
+                               p.O - 1);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = acc[j][i];
-          if (mine && o < p.O) put8(p, base, row, o, v);
-        }
-      }
-    } else {
-      // 64 columns, in pairs of tiles whose results give a lane eight neighbours.
-      for (int o0 = begin + 64 * wave; o0 < end; o0 += 64 * kWaves) {
-        v4f acc[2][2] = {};
-        for (int s = 0; s < steps; ++s) {
-          int chunk;
-          const v4u h = part(s, chunk);
-          v4u wv[2][2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int o = min(o0 + 32 * q + 8 * (l >> 2) + 4 * j + (l & 3), p.O - 1);
-              wv[q][j] = *reinterpret_cast<const v4u*>(w + (size_t)o * p.R + 8 * chunk);
-            }
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) acc[q][j] = multiply_bf16(wv[q][j], h, acc[q][j]);
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int o = o0 + 32 * q + 8 * g;
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = acc[q][i / 4][i % 4];
-          if (mine && o < p.O) put8(p, base, row, o, v);
+            for (int i = 0; i < kLoads; ++i)
+              wv[s][kLoads * j + i] = *reinterpret_cast<const v4u*>(
+                  w + (size_t)at * p.R + min(rank0 + (sizeof(T) == 2 ? 8 * g : 16 * i + 4 * g), p.R - 16 / (int)sizeof(T)));
+          }
         }
       }
-    }
-  } else if constexpr (ACROSS) {
-    // 64 columns: lane l reads four of them, which four tiles share.
-    for (int o0 = begin + 64 * wave; o0 < end; o0 += 64 * kWaves) {
-      v4f acc[4] = {};
-      for (int r = g; live && r < p.R; r += 4) {
-        const float h = *reinterpret_cast<const float*>(s_hidden + l * pitch + 4 * r);
-        const v4f wv = *reinterpret_cast<const v4f*>(w + (size_t)r * p.O + min(o0 + 4 * l, p.O - 4));
+    };
+    // acc[j]: column(j, i) of row l of the tile
+    const auto multiply = [&](int t, int block, v4f (&acc)[kCols]) {
+      const uint8_t* const h_row = s_hidden + (kTile * t + l) * pitch;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(wv[j], h, acc[j], 0, 0, 0);
-      }
+      for (int s = 0; s < STEPS; ++s) {
+        const int rank0 = kRanks * (STEPS * block + s);
+        if (rank0 >= p.R) break;
+        if constexpr (sizeof(T) == 2) {
+          const int r = rank0 + 8 * g, at = min(r, p.R - 8);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int o = o0 + 4 * (4 * g + i);
-        if (mine && o < p.O) put4(p, base, row, o, v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]});
-      }
-    }
-  } else {
-    for (int o0 = begin + 64 * wave; o0 < end; o0 += 64 * kWaves) {
-      v4f acc[4] = {};
-      for (int r0 = 0; live && r0 < p.R; r0 += 16) {
-        const int r = r0 + 4 * g, at = min(r, p.R - 4);
-        v4f h = *reinterpret_cast<const v4f*>(s_hidden + l * pitch + 4 * at);
-        if (r >= p.R) h = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int d = 0; d < 2; ++d) {          // high and low parts
+            v4u h = *reinterpret_cast<const v4u*>(h_row + d * (TT * kTile) * pitch + 2 * at);
+            if (r >= p.R) h = v4u{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const v4f wv = *reinterpret_cast<const v4f*>(w + (size_t)min(o0 + 16 * j + l, p.O - 1) * p.R + at);
+            for (int j = 0; j < kCols; ++j) acc[j] = multiply_bf16(wv[s][j], h, acc[j]);
+          }
+        } else if constexpr (ACROSS) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(wv[i], h[i], acc[j], 0, 0, 0);
+          for (int i = 0; i < 8; ++i) {
+            const int r = rank0 + 4 * i + g;
+            float h = *reinterpret_cast<const float*>(h_row + 4 * min(r, p.R - 1));
+            h = r < p.R ? h : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+              acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(wv[s][i][j]), h, acc[j], 0, 0, 0);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            const int r = rank0 + 16 * i + 4 * g;
+            v4f h = *reinterpret_cast<const v4f*>(h_row + 4 * min(r, p.R - 4));
+            if (r >= p.R) h = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(wv[s][kLoads * j + i][e]), h[e], acc[j], 0, 0, 0);
+          }
         }
       }
+    };
+    if constexpr (KEPT) load_w(0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int o = o0 + 16 * j + 4 * g;
-        if (mine && o < p.O) put4(p, base, row, o, acc[j]);
+    for (int t = 0; t < TT; ++t) {
+      if (t >= tiles) continue;
+      v4f acc[kCols] = {};
+      if constexpr (KEPT) {
+        if (live) multiply(t, 0, acc);
+      } else {
+        for (int block = 0; block < blocks; ++block) {
+          load_w(block);
+          multiply(t, block, acc);
+        }
+      }
+      wave_sync();
+      if constexpr (ACROSS) {
+        // column(j, i) = 4 (4 g + i) + j
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          bounce.at(sizeof(T) == 2 ? i % 2 : 0, l, sizeof(T) == 2 ? 2 * g + i / 2 : 4 * g + i) =
+              v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+      } else {
+        // column(j, i) = 32 (j / 2) + 8 g + 4 (j % 2) + i (bf16), 16 j + 4 g + i (float)
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          if constexpr (sizeof(T) == 2) bounce.at(j % 2, l, 4 * (j / 2) + g) = acc[j];
+          else bounce.at(0, l, 4 * j + g) = acc[j];
+        }
+      }
+      wave_sync();
+#pragma unroll
+      for (int k = 0; k < B::kPasses; ++k) {
+        const int i = B::kRows * k + pass_row;
+        const v4f v = bounce.at(0, i, piece);
+        if constexpr (sizeof(T) == 2) {
+          const v4f u = bounce.at(1, i, piece);
+          const v4u b = base[t][k];
+          uint16_t r[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            r[e] = rounded<uint16_t>((e < 4 ? v[e % 4] : u[e % 4]) +
+                                     __uint_as_float(e & 1 ? b[e / 2] & 0xFFFF0000u : b[e / 2] << 16));
+          put<uint16_t>(p, row_of(t, k), o, r);
+        } else {
+          const v4f sum = v + __builtin_bit_cast(v4f, base[t][k]);
+          float r[4];
+          __builtin_memcpy(r, &sum, 16);
+          put<float>(p, row_of(t, k), o, r);
+        }
       }
     }
   }
 }
 
 // grid: slices of the results or parts of the sum, tiles of a window, windows.
-template <class T, int NR, bool ACROSS, int STAGE>
-__global__ __launch_bounds__(kThreads) void rows_kernel(RowsParams p) {
-  __shared__ Rows s_rows;
-  __shared__ __align__(16) uint8_t s_sum[STAGE == kExpand ? 16 : kSumBytes<T, NR, ACROSS>];
-  __shared__ __align__(16) uint8_t s_hidden[STAGE == kShrink ? 16 : kHiddenBytes];
-  if (!group_rows(p.ids, p.M, p.n, (int)blockIdx.z, (int)blockIdx.y, s_rows)) return;
-  const int adapter = s_rows.adapter, count = s_rows.count;
+// TT: tiles of 16 rows of a work-group.
+template <class T, int NR, bool ACROSS, int STAGE, int TT>
+__global__ __launch_bounds__(kThreads, TT == 1 && NR < 8 && !(ACROSS && sizeof(T) == 2) ? 4 : 2) void rows_kernel(RowsParams p) {
+  // the waves' sums of the first product, then the results of the second
+  constexpr int kSum = STAGE == kExpand ? 0 : kSumBytes<T, NR, ACROSS>;
+  constexpr int kOut = STAGE == kShrink ? 0 : kWaves * Bounce<T>::kBytes;
+  __shared__ __align__(16) uint8_t s_sum[kSum > kOut ? kSum : kOut];
+  __shared__ __align__(16) uint8_t s_hidden[STAGE == kShrink ? 16 : kHiddenBytes<NR, TT>];
+  const Rows rows = group_rows<TT * kTile>(p.ids, p.M, p.n, (int)blockIdx.z, (int)blockIdx.y);
+  const int adapter = rows.adapter, count = rows.count;
+  if (!count) return;
   const bool live = adapter >= 0;
   const size_t table = (size_t)max(adapter, 0) * p.R;
   const float scale = live && p.scales ? p.scales[adapter] : 1.0f;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tiles = (count + kTile - 1) / kTile;
   const bool first = blockIdx.x == 0;
   // four sums of a row, complete
   const auto finish = [&](int row, int r, v4f v) {
     if (row >= count || r >= p.R) return;
     const v4f scaled = v * scale;
-    if (p.hidden && first) *reinterpret_cast<v4f*>(p.hidden + (size_t)s_rows.row[row] * p.R + r) = ACROSS ? scaled : v;
-    keep_hidden<T>(s_hidden, p.R, row, r, scaled);
+    if (p.hidden && first) *reinterpret_cast<v4f*>(p.hidden + (size_t)rows.row(row) * p.R + r) = ACROSS ? scaled : v;
+    keep_hidden<T, TT>(s_hidden, p.R, row, r, scaled);
   };
   if constexpr (STAGE != kExpand) {
     const int steps = (p.C + kStep<T, NR, ACROSS> - 1) / kStep<T, NR, ACROSS>;
     const int split = STAGE == kShrink ? (int)blockIdx.x : 0, splits = STAGE == kShrink ? p.splits : 1;
     const int begin = (int)((int64_t)steps * split / splits), end = (int)((int64_t)steps * (split + 1) / splits);
     v4f(*const sums)[NR][64] = reinterpret_cast<v4f(*)[NR][64]>(s_sum);
-    for (int rank0 = 0; rank0 < p.R; rank0 += kRankBlock) {
-      v4f acc[NR] = {};
-      if (live)
-        shrink_rows<T, NR, ACROSS>(p, static_cast<const T*>(p.shrink) + table * p.C, s_rows.row[min(lane & 15, count - 1)],
-                                   rank0, begin, end, s_sum, acc);
-      __syncthreads();
+    int row[TT];
 #pragma unroll
-      for (int j = 0; j < NR; ++j) sums[wave][j][lane] = acc[j];
-      __syncthreads();
-      for (int i = threadIdx.x; i < NR * 64; i += kThreads) {
-        const int j = i >> 6, from = i & 63, row = from & 15, r = rank0 + 16 * j + 4 * (from >> 4);
-        v4f v = sums[0][j][from];
-        for (int k = 1; k < kWaves; ++k) v += sums[k][j][from];
-        if constexpr (STAGE == kBoth) {
-          finish(row, r, v);
-        } else if (row < count && r < p.R) {
-          *reinterpret_cast<v4f*>(p.partial + ((size_t)split * p.M + s_rows.row[row]) * p.R + r) = v;
+    for (int t = 0; t < TT; ++t) row[t] = rows.row(min(kTile * t + (lane & 15), count - 1));
+    for (int rank0 = 0; rank0 < p.R; rank0 += kRankBlock) {
+      v4f acc[TT][NR] = {};
+      if (live)
+        shrink_rows<T, NR, ACROSS, TT>(p, static_cast<const T*>(p.shrink) + table * p.C, row, tiles, rank0, begin, end, s_sum,
+                                       acc);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        if (t >= tiles) break;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NR; ++j) sums[wave][j][lane] = acc[t][j];
+        __syncthreads();
+        for (int i = threadIdx.x; i < NR * 64; i += kThreads) {
+          const int j = i >> 6, from = i & 63, at = kTile * t + (from & 15), r = rank0 + 16 * j + 4 * (from >> 4);
+          v4f v = sums[0][j][from];
+          for (int k = 1; k < kWaves; ++k) v += sums[k][j][from];
+          if constexpr (STAGE == kBoth) {
+            finish(at, r, v);
+          } else if (at < count && r < p.R) {
+            *reinterpret_cast<v4f*>(p.partial + ((size_t)split * p.M + rows.row(at)) * p.R + r) = v;
+          }
         }
       }
       __syncthreads();
     }
   } else {
-    for (int i = threadIdx.x; i < kTile * p.R / 4; i += kThreads) {
+    for (int i = threadIdx.x; i < TT * kTile * p.R / 4; i += kThreads) {
       const int row = i / (p.R / 4), r = 4 * (i % (p.R / 4));
       if (row >= count) break;
-      const float* const at = p.partial + (size_t)s_rows.row[row] * p.R + r;
+      const float* const at = p.partial + (size_t)rows.row(row) * p.R + r;
       v4f v = *reinterpret_cast<const v4f*>(at);
       for (int k = 1; k < p.splits; ++k) v += *reinterpret_cast<const v4f*>(at + (size_t)k * p.M * p.R);
       finish(row, r, v);
@@ -437,65 +580,73 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsParams p) {
   if constexpr (STAGE != kShrink) {
     if (!p.out) return;
     const int begin = (int)blockIdx.x * p.slice, end = min(p.O, begin + p.slice);
-    expand_rows<T, ACROSS>(p, static_cast<const T*>(p.expand) + table * p.O, live, s_rows, s_hidden, begin, end);
+    const T* const w = static_cast<const T*>(p.expand) + table * p.O;
+    // two blocks of 32 ranks and 64 registers are kept at most
+    constexpr int kSteps = TT > 1 && NR == 4 ? 2 : 1;
+    expand_rows<T, kSteps, (TT > 1 && NR <= 4), ACROSS, TT>(p, w, live, rows, s_hidden, s_sum, begin, end);
   }
 }
 
 // Kernels by type, tiles of 16 ranks in a pass, and direction.
-template <class T, bool ACROSS, int STAGE>
+template <class T, bool ACROSS, int STAGE, int TT>
 const void* pick(int R) {
-  if constexpr (STAGE != kExpand) {
-    if (R > 64) return reinterpret_cast<const void*>(&rows_kernel<T, 8, ACROSS, STAGE>);
-    if (R > 32) return reinterpret_cast<const void*>(&rows_kernel<T, 4, ACROSS, STAGE>);
-    if (R > 16) return reinterpret_cast<const void*>(&rows_kernel<T, 2, ACROSS, STAGE>);
-  }
-  return reinterpret_cast<const void*>(&rows_kernel<T, 1, ACROSS, STAGE>);
+  if (R > 64) return reinterpret_cast<const void*>(&rows_kernel<T, 8, ACROSS, STAGE, TT>);
+  if (R > 32) return reinterpret_cast<const void*>(&rows_kernel<T, 4, ACROSS, STAGE, TT>);
+  if (R > 16) return reinterpret_cast<const void*>(&rows_kernel<T, 2, ACROSS, STAGE, TT>);
+  return reinterpret_cast<const void*>(&rows_kernel<T, 1, ACROSS, STAGE, TT>);
 }
-template <int STAGE>
-const void* pick(int R, bool f32, bool across) {
-  if (f32) return across ? pick<float, true, STAGE>(R) : pick<float, false, STAGE>(R);
-  return across ? pick<uint16_t, true, STAGE>(R) : pick<uint16_t, false, STAGE>(R);
-}
-
-template <int STAGE>
+template <int STAGE, int TT>
 hipError_t launch(RowsParams p, int blocks, bool f32, bool across, hipStream_t stream) {
+  const void* const kernel = f32 ? across ? pick<float, true, STAGE, TT>(p.R) : pick<float, false, STAGE, TT>(p.R)
+                                 : across ? pick<uint16_t, true, STAGE, TT>(p.R) : pick<uint16_t, false, STAGE, TT>(p.R);
   void* args[] = {&p};
-  const dim3 grid((unsigned)blocks, (unsigned)window_tiles(p.M, p.n, p.ids != nullptr),
+  const dim3 grid((unsigned)blocks, (unsigned)window_tiles(p.M, p.n, p.ids != nullptr, TT * kTile),
                   (unsigned)((p.M + kWindow - 1) / kWindow));
-  return hipLaunchKernel(pick<STAGE>(p.R, f32, across), grid, dim3(kThreads), args, 0, stream);
+  return hipLaunchKernel(kernel, grid, dim3(kThreads), args, 0, stream);
 }
 
-// Work-groups along the results: as many as fill the device, of 512 columns (one
-// unit of each wave) at least.
-int slices_for(int M, int O, int& slice) {
-  const int tiles = (M + kTile - 1) / kTile, most = (O + 511) / 512;
-  int s = (kFill / 2 + tiles - 1) / tiles;
+// Work-groups along the results: as many as make `fill` of them, of one unit of
+// each wave at least.
+int slices_for(const RowsParams& p, int tiles, int fill, int& slice) {
+  constexpr int unit = kWaves * kUnit;
+  const int most = p.out ? (p.O + unit - 1) / unit : 1;
+  int s = (fill + tiles - 1) / tiles;
   s = s > most ? most : s;
-  slice = ((O + s - 1) / s + 511) / 512 * 512;
-  return (O + slice - 1) / slice;
+  slice = ((p.O + s - 1) / s + unit - 1) / unit * unit;
+  return p.out ? (p.O + slice - 1) / slice : 1;
+}
+
+// Parts of the long sum.
+int splits_for(const RowsParams& p, int tiles, int fill) {
+  const int steps = (p.C + 511) / 512;
+  int s = fill / tiles;
+  s = s > kMaxSplits ? kMaxSplits : s;
+  s = s > steps ? steps : s;
+  return s < 1 ? 1 : s;
 }
 
 hipError_t launch_rows(RowsParams p, bool f32, bool across, hipStream_t stream) {
-  const int tiles = (p.M + kTile - 1) / kTile, steps = (p.C + 511) / 512;
-  int slices = slices_for(p.M, p.O, p.slice);
-  if (!p.out) slices = 1;
-  int splits = kFill / tiles;
-  splits = splits > kMaxSplits ? kMaxSplits : splits;
-  splits = splits > steps ? steps : splits;
-  const size_t table = (size_t)p.R * p.C * (f32 ? 4 : 2);
-  if (splits <= 1 || table <= (1u << 18)) {
-    p.splits = 1;
-    return launch<kBoth>(p, slices, f32, across, stream);
+  if (p.M >= kLargeBatch) {
+    const int tiles = (p.M + 63) / 64;
+    p.splits = splits_for(p, tiles, kFill);
+    const hipError_t e = launch<kShrink, 4>(p, p.splits, f32, across, stream);
+    if (e != hipSuccess) return e;
+    const int slices = slices_for(p, tiles, 2 * kFill, p.slice);
+    return launch<kExpand, 4>(p, slices, f32, across, stream);
   }
-  p.splits = splits;
-  const hipError_t e = launch<kShrink>(p, splits, f32, across, stream);
-  return e != hipSuccess ? e : launch<kExpand>(p, slices, f32, across, stream);
+  const int tiles = (p.M + kTile - 1) / kTile;
+  const int slices = slices_for(p, tiles, kFill / 2, p.slice);
+  p.splits = splits_for(p, tiles, kFill);
+  const size_t table = (size_t)p.R * p.C * (f32 ? 4 : 2);
+  if (p.splits == 1 || table <= (1u << 18)) return launch<kBoth, 1>(p, slices, f32, across, stream);
+  const hipError_t e = launch<kShrink, 1>(p, p.splits, f32, across, stream);
+  return e != hipSuccess ? e : launch<kExpand, 1>(p, slices, f32, across, stream);
 }
 
 // The parts of the hidden sums: M rows, or while there are several parts at
-// most kFill tiles in all.
+// most kFill tiles of 64 rows in all.
 size_t hidden_bytes(int64_t M, int64_t R) {
-  const int64_t several = M * kMaxSplits < kFill * kTile ? M * kMaxSplits : kFill * kTile;
+  const int64_t several = M * kMaxSplits < kFill * 64 ? M * kMaxSplits : kFill * 64;
   const size_t rows = (size_t)(M > several ? M : several);
   return (rows * (size_t)R * 4 + 255) / 256 * 256;
 }
