@@ -61,6 +61,57 @@ __device__ __forceinline__ int adapter_of(const int32_t* ids, int row, int n) {
   return (uint32_t)id < (uint32_t)n ? id : -1;
 }
 
+// A work-group of eight waves sorts out an adapter's rows: where they begin among
+// those sorted by adapter, and the rows.  Each wave takes a run of the rows; it is
+// read twice, first to count.  No atomics: the same order on every run.
+__device__ __forceinline__ void order_rows(const int32_t* ids, int M, int n, int adapter, int32_t* order,
+                                           int32_t* offsets) {
+  constexpr int kWaves = 8, kAhead = 8;
+  __shared__ int s_below[kWaves], s_mine[kWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int steps = (M + 63) / 64, begin = 64 * (steps * wave / kWaves), end = min(M, 64 * (steps * (wave + 1) / kWaves));
+  const auto visit = [&](auto&& see) {
+    for (int t0 = begin; t0 < end; t0 += 64 * kAhead) {
+      int id[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) id[k] = ids[min(t0 + 64 * k + lane, M - 1)];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int t = t0 + 64 * k + lane;
+        see(t, t < end ? id[k] : -1);
+      }
+    }
+  };
+  int below = 0, mine = 0;
+  visit([&](int, int id) {
+    below += __popcll(__ballot(id >= 0 && id < adapter));
+    mine += __popcll(__ballot(id == adapter));
+  });
+  if (lane == 0) {
+    s_below[wave] = below;
+    s_mine[wave] = mine;
+  }
+  __syncthreads();
+  int start = 0, at = 0, count = 0;
+  for (int w = 0; w < kWaves; ++w) {
+    start += s_below[w];
+    at += w < wave ? s_mine[w] : 0;
+    count += s_mine[w];
+  }
+  if (threadIdx.x == 0) {
+    offsets[adapter] = start;
+    if (adapter == n - 1) offsets[n] = start + count;
+  }
+  if (!mine) return;
+  at += start;
+  visit([&](int t, int id) {
+    const uint64_t votes = __ballot(id == adapter);
+    if (id == adapter) order[at + __popcll(votes & ((1ull << lane) - 1))] = t;
+    at += __popcll(votes);
+  });
+}
+
 // The gradients of the matrices.  `order` are the rows that have an adapter,
 // by adapter and then in their own order, `offsets` [n + 1] where each adapter's
 // begin; without ids neither is used.
@@ -77,6 +128,7 @@ struct AdapterGradParams {
   int32_t* offsets;
   float* parts;           // sums of adapters whose rows several work-groups share
   int M, N, K, R, n, xf32;
+  bool sorted;            // order and offsets are there
 };
 
 size_t adapter_grad_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t n);

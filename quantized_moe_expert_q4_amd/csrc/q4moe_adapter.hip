@@ -138,6 +138,8 @@ struct RowsParams {
   int M, C, O, R, n;
   int splits;             // parts of the long sum
   int slice;              // columns of a work-group's results
+  int32_t* order;         // or nullptr: the work-groups past the windows sort the rows
+  int32_t* offsets;
 };
 
 // What a launch does: all of it, or one of the two products.
@@ -216,34 +218,44 @@ __device__ __forceinline__ void shrink_rows(const RowsParams& p, const T* w, con
     for (int s = begin + wave; s < end; s += kWaves) {
       const int c0 = s * kCount;
       const bool whole = c0 + kCount <= p.C;
-      const auto load_x = [&](int h, v4u (&xv)[TT]) {
+      // as much on its way at once as 64 registers hold
+      constexpr int kSteps = kCount / 32, kAhead = kSteps * TT > 16 ? 16 / TT : kSteps;
+      v4u from[8], column[8], xv[kAhead][TT];
+      const auto load_x = [&](int h0) {
+        if (whole) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const int c = c0 + 32 * h + 8 * g;
-          if (whole) __builtin_memcpy(&xv[t], x.data + (size_t)row[t] * p.C + c, 16);
-          else xv[t] = x.chunk(row[t], c);
+          for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+              __builtin_memcpy(&xv[h][t], x.data + (size_t)row[t] * p.C + c0 + 32 * (h0 + h) + 8 * g, 16);
+        } else {
+#pragma unroll
+          for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) xv[h][t] = x.chunk(row[t], c0 + 32 * (h0 + h) + 8 * g);
         }
       };
-      v4u from[8], column[8], xv[2][TT];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         from[i] = *reinterpret_cast<const v4u*>(w + (size_t)min(c0 + 8 * part + i, p.C - 1) * p.R + rank);
-      load_x(0, xv[0]);
+      load_x(0);
       turn(from, column);
       wave_sync();
 #pragma unroll
       for (int i = 0; i < 8; ++i) s_w[place(8 * octet + i, part)] = column[i];
       wave_sync();
+#pragma unroll 1
+      for (int h0 = 0; h0 < kSteps; h0 += kAhead) {
+        if (h0) load_x(h0);
 #pragma unroll
-      for (int h = 0; h < kCount / 32; ++h) {
-        if (h + 1 < kCount / 32) load_x(h + 1, xv[(h + 1) & 1]);
+        for (int h = 0; h < kAhead; ++h)
 #pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          const v4u wv = s_w[place(16 * j + l, 4 * h + g)];
+          for (int j = 0; j < NR; ++j) {
+            const v4u wv = s_w[place(16 * j + l, 4 * (h0 + h) + g)];
 #pragma unroll
-          for (int t = 0; t < TT; ++t)
-            if (t < tiles) acc[t][j] = multiply_bf16(wv, xv[h & 1][t], acc[t][j]);
-        }
+            for (int t = 0; t < TT; ++t)
+              if (t < tiles) acc[t][j] = multiply_bf16(wv, xv[h][t], acc[t][j]);
+          }
       }
     }
   } else {
@@ -517,6 +529,15 @@ __global__ __launch_bounds__(kThreads, TT == 1 && NR < 8 && !(ACROSS && sizeof(T
   constexpr int kOut = STAGE == kShrink ? 0 : kWaves * Bounce<T>::kBytes;
   __shared__ __align__(16) uint8_t s_sum[kSum > kOut ? kSum : kOut];
   __shared__ __align__(16) uint8_t s_hidden[STAGE == kShrink ? 16 : kHiddenBytes<NR, TT>];
+  if constexpr (STAGE != kExpand) {
+    if ((int)blockIdx.z * kWindow >= p.M) {
+      for (int i = (int)(blockIdx.x + blockIdx.y * gridDim.x); i < p.n; i += (int)(gridDim.x * gridDim.y)) {
+        order_rows(p.ids, p.M, p.n, i, p.order, p.offsets);
+        __syncthreads();
+      }
+      return;
+    }
+  }
   const Rows rows = group_rows<TT * kTile>(p.ids, p.M, p.n, (int)blockIdx.z, (int)blockIdx.y);
   const int adapter = rows.adapter, count = rows.count;
   if (!count) return;
@@ -601,7 +622,7 @@ hipError_t launch(RowsParams p, int blocks, bool f32, bool across, hipStream_t s
                                  : across ? pick<uint16_t, true, STAGE, TT>(p.R) : pick<uint16_t, false, STAGE, TT>(p.R);
   void* args[] = {&p};
   const dim3 grid((unsigned)blocks, (unsigned)window_tiles(p.M, p.n, p.ids != nullptr, TT * kTile),
-                  (unsigned)((p.M + kWindow - 1) / kWindow));
+                  (unsigned)((p.M + kWindow - 1) / kWindow + (STAGE != kExpand && p.order ? 1 : 0)));
   return hipLaunchKernel(kernel, grid, dim3(kThreads), args, 0, stream);
 }
 
@@ -658,20 +679,23 @@ size_t adapter_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t n) 
 }
 
 hipError_t launch_adapter(const AdapterParams& p, hipStream_t stream) {
-  return launch_rows({p.x, p.a, p.b, p.ids, p.scales, p.base, p.out, p.hidden, p.partial, p.M, p.K, p.N, p.R, p.n, 0, 0},
+  return launch_rows({p.x, p.a, p.b, p.ids, p.scales, p.base, p.out, p.hidden, p.partial, p.M, p.K, p.N, p.R, p.n, 0, 0, nullptr, nullptr},
                      p.xf32, false, stream);
 }
 
 hipError_t launch_adapter_backward(const AdapterBackwardParams& p, hipStream_t stream) {
   float* const g = p.partial + hidden_bytes(p.M, p.R) / 4;
   float* const rest = g + (size_t)p.M * p.R / 64 * 64 + 64;
+  int32_t* const order = reinterpret_cast<int32_t*>(rest);
+  int32_t* const offsets = order + ((size_t)p.M + 63) / 64 * 64;
+  const bool grads = p.d_a || p.d_b, sorting = p.ids && grads;
   if (p.d_x || p.d_a) {
     const hipError_t e = launch_rows({p.d_out, p.b, p.a, p.ids, p.scales, p.base, p.d_x, p.d_a ? g : nullptr, p.partial,
-                                      p.M, p.N, p.K, p.R, p.n, 0, 0},
+                                      p.M, p.N, p.K, p.R, p.n, 0, 0, sorting ? order : nullptr, offsets},
                                      p.xf32, true, stream);
     if (e != hipSuccess) return e;
   }
-  if (!p.d_a && !p.d_b) return hipSuccess;
+  if (!grads) return hipSuccess;
   AdapterGradParams q{};
   q.x = p.x;
   q.d_out = p.d_out;
@@ -681,9 +705,10 @@ hipError_t launch_adapter_backward(const AdapterBackwardParams& p, hipStream_t s
   q.scales = p.scales;
   q.d_a = p.d_a;
   q.d_b = p.d_b;
-  q.order = reinterpret_cast<int32_t*>(rest);
-  q.offsets = q.order + ((size_t)p.M + 63) / 64 * 64;
-  q.parts = reinterpret_cast<float*>(q.offsets + ((size_t)p.n + 64) / 64 * 64);
+  q.order = order;
+  q.offsets = offsets;
+  q.sorted = p.d_x || p.d_a;
+  q.parts = reinterpret_cast<float*>(offsets + ((size_t)p.n + 64) / 64 * 64);
   q.M = p.M;
   q.N = p.N;
   q.K = p.K;

@@ -2,8 +2,8 @@
 //   d_a[r][k] = sum_t g[t][r] x[t][k],   d_b[n][r] = s sum_t d_out[t][n] hidden[t][r],
 // over the rows t of each adapter.
 //
-// The rows are sorted by adapter first (order_kernel, without atomics: the same
-// order on every run) and cut into chunks of `rows`.  A work-group takes a slice
+// The rows are sorted by adapter first (order_rows, beside the call's first
+// product where it has one) and cut into chunks of `rows`.  A work-group takes a slice
 // of the long dimension and a chunk: its eight waves each take 32 rows at a time,
 // read 16 bytes of each (whole runs of 256 bytes), turn them in registers into
 // matrix operands along the rows, and multiply them with the short vectors, which
@@ -20,62 +20,18 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRanks = 32;           // ranks of a wave at most: more sums would not fit its registers
-constexpr int kFill = 512;           // work-groups that fill the device: no more chunks than give so many
+constexpr int kTogether = 4;         // tiles of sums that the waves join at a time
+constexpr int kFill = 256;           // work-groups that the device runs at a time: no more chunks than give so many
 constexpr int kLeastRows = 256;      // rows that a chunk has at least: 32 of each wave
 
 // Columns of a work-group's slice.
 template <class T>
 constexpr int kColumns = 256 / (int)sizeof(T);
 
-// A work-group for each adapter: where its rows begin among the sorted ones, and
-// the rows.  Each wave takes a run of the rows; it is read twice, first to count.
+// The sorting alone, for a call that has no product of rows to do beside it.
 __global__ __launch_bounds__(kThreads) void order_kernel(const int32_t* ids, int M, int n, int32_t* order,
                                                          int32_t* offsets) {
-  constexpr int kAhead = 8;
-  __shared__ int s_below[kWaves], s_mine[kWaves];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int adapter = (int)blockIdx.x;
-  const int steps = (M + 63) / 64, begin = 64 * (steps * wave / kWaves), end = min(M, 64 * (steps * (wave + 1) / kWaves));
-  const auto visit = [&](auto&& see) {
-    for (int t0 = begin; t0 < end; t0 += 64 * kAhead) {
-      int id[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) id[k] = ids[min(t0 + 64 * k + lane, M - 1)];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int t = t0 + 64 * k + lane;
-        see(t, t < end ? id[k] : -1);
-      }
-    }
-  };
-  int below = 0, mine = 0;
-  visit([&](int, int id) {
-    below += __popcll(__ballot(id >= 0 && id < adapter));
-    mine += __popcll(__ballot(id == adapter));
-  });
-  if (lane == 0) {
-    s_below[wave] = below;
-    s_mine[wave] = mine;
-  }
-  __syncthreads();
-  int start = 0, at = 0, count = 0;
-  for (int w = 0; w < kWaves; ++w) {
-    start += s_below[w];
-    at += w < wave ? s_mine[w] : 0;
-    count += s_mine[w];
-  }
-  if (threadIdx.x == 0) {
-    offsets[adapter] = start;
-    if (adapter == n - 1) offsets[n] = start + count;
-  }
-  if (!mine) return;
-  at += start;
-  visit([&](int t, int id) {
-    const uint64_t votes = __ballot(id == adapter);
-    if (id == adapter) order[at + __popcll(votes & ((1ull << lane) - 1))] = t;
-    at += __popcll(votes);
-  });
+  order_rows(ids, M, n, (int)blockIdx.x, order, offsets);
 }
 
 // One of the two gradients: y's columns against h's ranks.
@@ -108,7 +64,7 @@ __device__ __forceinline__ int row_of(int lane_group, int i) {
 // NR: tiles of 16 ranks of a wave.
 template <class T, int NR, bool IS_A>
 __device__ __forceinline__ void grad_slice(const GradLaunch& p, const Grad& q, int slice, int chunk,
-                                           v4f (*s_sum)[NR][64]) {
+                                           v4f (*s_sum)[kWaves][NR][64]) {
   constexpr int kVec = 16 / sizeof(T);           // columns of a lane, one in each of as many tiles of 16
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -132,13 +88,19 @@ __device__ __forceinline__ void grad_slice(const GradLaunch& p, const Grad& q, i
     // and ranks other values come along, whose results are not stored.
     v4u rows[8];
     float h[NR][8];
-    int t[8];
-    auto fetch_rows = [&](int at) {
+    int t[8], next_t[8];             // the rows' numbers are known a step earlier
+    auto fetch_numbers = [&](int at, int (&t)[8]) {
+      if (!p.ids) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int pos = min(at + row_of<T>(g, i), end - 1);
-        t[i] = p.ids ? p.order[pos] : pos;
+        for (int i = 0; i < 8; ++i) t[i] = min(at + row_of<T>(g, i), end - 1);
+      } else if (sizeof(T) == 2 && at + 32 <= end) {
+        __builtin_memcpy(t, p.order + at + 8 * g, 32);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = p.order[min(at + row_of<T>(g, i), end - 1)];
       }
+    };
+    auto fetch_rows = [&]() {
 #pragma unroll
       for (int i = 0; i < 8; ++i) rows[i] = y.load(t[i], col);
       if (ragged) {
@@ -157,7 +119,9 @@ __device__ __forceinline__ void grad_slice(const GradLaunch& p, const Grad& q, i
     };
     int at = rank0 < p.R ? begin + 32 * (wave >> p.shift) : end;
     if (at < end) {
-      fetch_rows(at);
+      fetch_numbers(at, t);
+      fetch_numbers(at + step, next_t);
+      fetch_rows();
 #pragma unroll
       for (int j = 0; j < NR; ++j) fetch_ranks(at, j);
     }
@@ -170,7 +134,12 @@ __device__ __forceinline__ void grad_slice(const GradLaunch& p, const Grad& q, i
 #pragma unroll
         for (int i = 0; i < 8; ++i) column[i] = rows[i];
       }
-      if (next < end) fetch_rows(next);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = next_t[i];
+      if (next < end) {
+        fetch_rows();
+        fetch_numbers(next + step, next_t);
+      }
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
         if constexpr (sizeof(T) == 2) {
@@ -199,30 +168,33 @@ __device__ __forceinline__ void grad_slice(const GradLaunch& p, const Grad& q, i
       }
       at = next;
     }
-    // the waves' sums, tile by tile
+    // the waves' sums
     const float scale = q.scales ? q.scales[adapter] : 1.0f;
     float* const out = several ? q.parts + (size_t)(2 * chunk + (begin == chunk_begin ? 0 : 1)) * q.O * p.R
                                : q.out + (size_t)adapter * q.O * p.R;
 #pragma unroll
-    for (int c = 0; c < kVec; ++c) {
+    for (int c0 = 0; c0 < kVec; c0 += kTogether) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < NR; ++j) s_sum[wave][j][lane] = acc[c][j];
+      for (int c = 0; c < kTogether; ++c)
+#pragma unroll
+        for (int j = 0; j < NR; ++j) s_sum[c][wave][j][lane] = acc[c0 + c][j];
       __syncthreads();
-      for (int i = threadIdx.x; i < (NR * 64) << p.shift; i += kThreads) {
-        const int tile = i >> 6, j = tile % NR, first = tile / NR, from = i & 63, fl = from & 15, fg = from >> 4;
-        v4f v = s_sum[first][j][from];
-        for (int w = first + rank_waves; w < kWaves; w += rank_waves) v += s_sum[w][j][from];
+      for (int i = threadIdx.x; i < (kTogether * NR * 64) << p.shift; i += kThreads) {
+        const int c = i / 64 % kTogether, tile = i / (64 * kTogether), j = tile % NR, first = tile / NR;
+        const int from = i & 63, fl = from & 15, fg = from >> 4;
+        v4f v = s_sum[c][first][j][from];
+        for (int w = first + rank_waves; w < kWaves; w += rank_waves) v += s_sum[c][w][j][from];
         v *= scale;
         if constexpr (IS_A) {
           const int r = 16 * tile + fl;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int o = o0 + kVec * (4 * fg + e) + c;
+            const int o = o0 + kVec * (4 * fg + e) + c0 + c;
             if (r < p.R && o < q.O) out[(size_t)r * q.O + o] = v[e];
           }
         } else {
-          const int r = 16 * tile + 4 * fg, o = o0 + kVec * fl + c;
+          const int r = 16 * tile + 4 * fg, o = o0 + kVec * fl + c0 + c;
           if (r < p.R && o < q.O) *reinterpret_cast<v4f*>(out + (size_t)o * p.R + r) = v;
         }
       }
@@ -233,7 +205,7 @@ __device__ __forceinline__ void grad_slice(const GradLaunch& p, const Grad& q, i
 
 template <class T, int NR>
 __global__ __launch_bounds__(kThreads, 2) void grad_kernel(GradLaunch p) {
-  __shared__ v4f s_sum[kWaves][NR][64];
+  __shared__ v4f s_sum[kTogether][kWaves][NR][64];
   int i = (int)blockIdx.x;
   if (i < p.a.slices * p.a.chunks) {
     grad_slice<T, NR, true>(p, p.a, i % p.a.slices, i / p.a.slices, s_sum);
@@ -244,40 +216,45 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(GradLaunch p) {
 }
 
 // The adapters that the chunks left: those of several chunks, and those without rows.
-__global__ __launch_bounds__(256) void join_kernel(GradLaunch p, Grad q) {
-  const size_t all = (size_t)q.O * p.R / 4, i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  for (int adapter = (int)blockIdx.y; adapter < p.n; adapter += (int)gridDim.y) {
-    const int begin = p.ids ? p.offsets[adapter] : adapter ? p.M : 0, end = p.ids ? p.offsets[adapter + 1] : p.M;
-    const int first = begin / q.rows, last = (end - 1) / q.rows;
-    if ((begin < end && first == last) || i >= all) continue;
-    v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (begin < end)
-      for (int c = first; c <= last; ++c) {
-        const int slot = 2 * c + (c == first && begin != c * q.rows ? 1 : 0);
-        sum += reinterpret_cast<const v4f*>(q.parts)[(size_t)slot * all + i];
-      }
-    reinterpret_cast<v4f*>(q.out)[(size_t)adapter * all + i] = sum;
+__global__ __launch_bounds__(256) void join_kernel(GradLaunch p, int blocks_a) {
+  const bool is_a = (int)blockIdx.x < blocks_a;
+  const Grad& q = is_a ? p.a : p.b;
+  const size_t all = (size_t)q.O * p.R / 4;
+  const size_t i = (size_t)((int)blockIdx.x - (is_a ? 0 : blocks_a)) * 256 + threadIdx.x;
+  const int adapter = (int)blockIdx.y;
+  const int begin = p.ids ? p.offsets[adapter] : adapter ? p.M : 0, end = p.ids ? p.offsets[adapter + 1] : p.M;
+  const int first = begin / q.rows, last = (end - 1) / q.rows;
+  if ((begin < end && first == last) || i >= all) return;
+  v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (begin < end) {
+#pragma unroll 4
+    for (int c = first; c <= last; ++c) {
+      const int slot = 2 * c + (c == first && begin != c * q.rows ? 1 : 0);
+      sum += reinterpret_cast<const v4f*>(q.parts)[(size_t)slot * all + i];
+    }
   }
+  reinterpret_cast<v4f*>(q.out)[(size_t)adapter * all + i] = sum;
 }
 
-int chunk_count(int M, int O, int columns) {
-  const int slices = (O + columns - 1) / columns, most = (M + kLeastRows - 1) / kLeastRows;
-  const int c = (kFill + slices - 1) / slices;
-  return c < most ? c : most;
+// 8192 rows of 4096 + 4096 columns, rank 16, in 2, 4, 8 and 16 chunks (128 to
+// 1024 work-groups): the backward call takes 110, 99, 107 and 117 us.
+int chunk_count(int M, int slices) {
+  const int most = (M + kLeastRows - 1) / kLeastRows, c = kFill / slices;
+  return c < 1 ? 1 : c < most ? c : most;
 }
 
-Grad grad_of(const AdapterGradParams& p, const void* y, const float* h, float* out, const float* scales, int O,
+Grad grad_of(const AdapterGradParams& p, const void* y, const float* h, float* out, const float* scales, int O, int slices,
              float* parts) {
   const int columns = p.xf32 ? kColumns<float> : kColumns<uint16_t>;
   Grad q{y, h, out, parts, scales, O, out ? (O + columns - 1) / columns : 0, 0, 0};
-  const int chunks = chunk_count(p.M, O, columns);
+  const int chunks = chunk_count(p.M, slices);
   q.rows = ((p.M + chunks - 1) / chunks + 31) / 32 * 32;
   q.chunks = (p.M + q.rows - 1) / q.rows;
   return q;
 }
 
-// Bytes of a gradient's parts, two for each chunk: chunk_count(M, O) * O is at
-// most the smaller of ceil(M / kLeastRows) * O and kFill * columns + O.
+// Bytes of a gradient's parts, two for each chunk: the chunks times O are at most
+// the smaller of ceil(M / kLeastRows) * O and kFill * columns + O.
 size_t part_bytes(int64_t M, int64_t O, int64_t R) {
   const int64_t by_rows = (M + kLeastRows - 1) / kLeastRows * O, by_fill = kFill * kColumns<uint16_t> + O;
   return (size_t)(by_rows < by_fill ? by_rows : by_fill) * (size_t)R * 8;
@@ -299,7 +276,7 @@ size_t adapter_grad_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_
 
 hipError_t launch_adapter_grad(const AdapterGradParams& p, hipStream_t stream) {
   hipError_t e = hipSuccess;
-  if (p.ids) {
+  if (p.ids && !p.sorted) {
     const int32_t* ids = p.ids;
     int M = p.M, n = p.n;
     int32_t *order = p.order, *offsets = p.offsets;
@@ -309,20 +286,27 @@ hipError_t launch_adapter_grad(const AdapterGradParams& p, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   float* const parts_a = p.parts + up(part_bytes(p.M, p.N, p.R)) / 4;
-  GradLaunch q{grad_of(p, p.x, p.g, p.d_a, nullptr, p.K, parts_a), grad_of(p, p.d_out, p.hidden, p.d_b, p.scales, p.N, p.parts),
+  const int columns = p.xf32 ? kColumns<float> : kColumns<uint16_t>;
+  const int slices = (p.d_a ? (p.K + columns - 1) / columns : 0) + (p.d_b ? (p.N + columns - 1) / columns : 0);
+  GradLaunch q{grad_of(p, p.x, p.g, p.d_a, nullptr, p.K, slices, parts_a),
+               grad_of(p, p.d_out, p.hidden, p.d_b, p.scales, p.N, slices, p.parts),
                p.ids, p.order, p.offsets, p.M, p.R, p.n, 0};
   while ((kRanks << q.shift) < p.R) ++q.shift;
   void* args[] = {&q};
   const unsigned blocks = (unsigned)(q.a.slices * q.a.chunks + q.b.slices * q.b.chunks);
   e = hipLaunchKernel(p.xf32 ? pick<float>(p.R) : pick<uint16_t>(p.R), dim3(blocks),
                       dim3(kThreads), args, 0, stream);
-  for (Grad* one : {&q.a, &q.b}) {
-    if (e != hipSuccess || !one->out || (!p.ids && p.n == 1 && one->chunks == 1)) continue;
-    void* join_args[] = {&q, one};
-    const size_t all = (size_t)one->O * p.R / 4;
-    e = hipLaunchKernel(reinterpret_cast<const void*>(&join_kernel), dim3((unsigned)((all + 255) / 256), (unsigned)p.n),
-                        dim3(256), join_args, 0, stream);
-  }
+  if (e != hipSuccess) return e;
+  const auto joins = [&](const Grad& g) {
+    const bool left = g.out && (p.ids || p.n > 1 || g.chunks > 1);
+    return left ? (int)(((size_t)g.O * p.R / 4 + 255) / 256) : 0;
+  };
+  int blocks_a = joins(q.a);
+  const int all = blocks_a + joins(q.b);
+  if (!all) return e;
+  void* join_args[] = {&q, &blocks_a};
+  e = hipLaunchKernel(reinterpret_cast<const void*>(&join_kernel), dim3((unsigned)all, (unsigned)p.n), dim3(256), join_args,
+                      0, stream);
   return e;
 }
 
