@@ -22,9 +22,9 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 256;
-constexpr int kCols = 128;           // columns k of a work-group
 constexpr int kChunks = 8;           // 16-byte chunks of a tile's row
+constexpr int kJoinThreads = 256;
+constexpr int kLarge = 200;          // tiles of 256 tokens from which on they are taken
 constexpr int kMaxSplits = 16;       // parts of n that work-groups share
 constexpr int kFill = 512;           // work-groups that fill the device: no more parts than give so many
 
@@ -45,18 +45,18 @@ __device__ __forceinline__ v4f multiply(const v4u a, const v4u b, v4f c) {
   }
 }
 
-template <bool F32>
-__device__ __forceinline__ float load_scale(const void* a, size_t i) {
-  if constexpr (F32) return static_cast<const float*>(a)[i];
-  else return bf16_val(static_cast<const uint16_t*>(a)[i]);
-}
-
-// T: the type of d_out as stored (uint16_t: bf16).  WM: waves along the tokens, 4 / WM along the columns.
-template <class T, int BM, int WM, bool AFF, bool SF>
-__global__ __launch_bounds__(kThreads) void linear_back_kernel(LinearBackParams p, int splits) {
-  constexpr int kVec = 16 / sizeof(T), kStep = kChunks * kVec, kWords = kStep / 16;
-  constexpr int MT = BM / WM / 16, KT = kCols / (4 / WM) / 16;     // 16 x 16 tiles of a wave
-  constexpr int kRows = BM / 32 ? BM / 32 : 1;                     // token chunks of a thread
+// T: the type of d_out as stored (uint16_t: bf16).  BM tokens by COLS columns, by
+// WAVES waves, WM of them along the tokens; AHEAD steps on their way.
+template <class T, int BM, int COLS, int WAVES, int WM, int AHEAD, bool AFF, bool SF>
+__global__ __launch_bounds__(64 * WAVES, 2) void linear_back_kernel(LinearBackParams p, int splits) {
+  constexpr int kThreads = 64 * WAVES, kCols = COLS;
+  constexpr int kVec = 16 / sizeof(T), kStep = kChunks * kVec;
+  constexpr int kWords = kStep * (COLS / 8) / kThreads;            // words of a thread: neighbouring rows n
+  constexpr int kLanes = kVec / kWords;                            // threads that fill a chunk
+  constexpr int MT = BM / WM / 16, KT = kCols / (WAVES / WM) / 16; // 16 x 16 tiles of a wave
+  constexpr int kSpan = kThreads / kChunks;                        // token rows that the threads load at a time
+  constexpr int kRows = BM / kSpan ? BM / kSpan : 1;               // token chunks of a thread
+  static_assert(kWords == 1 || kWords == 2 || kWords == 4, "a thread's weights at a column are written at once");
   __shared__ v4u s_d[2][BM * kChunks], s_w[2][kCols * kChunks];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -65,45 +65,71 @@ __global__ __launch_bounds__(kThreads) void linear_back_kernel(LinearBackParams 
   const int steps = (p.N + kStep - 1) / kStep;
   const int begin = (int)((int64_t)steps * blockIdx.z / splits), end = (int)((int64_t)steps * (blockIdx.z + 1) / splits);
 
-  // a thread's place among the weights: words of rows nq * kWords .. at the eight columns kb
-  const int kb = (tid >> 1) & 15, nq = (tid & 1) + 2 * (tid >> 5);
+  // a thread's place among the weights: words of rows nq * kWords .. at the eight
+  // columns kb; loads past the matrix give 0
+  const int kb = tid / kLanes % (kCols / 8), sub = tid % kLanes, chunk = tid / (kLanes * (kCols / 8));
+  const int nq = sub + kLanes * chunk;
   const bool col_in = k0 + 8 * kb < p.K;
-  const size_t pitch = (size_t)p.K / 8;                            // words of a row
-  const uint32_t* const w_at = reinterpret_cast<const uint32_t*>(p.w) + (k0 / 8 + (col_in ? kb : 0));
-  const int group = (k0 + (col_in ? 8 * kb : 0)) / p.group;
-
+  const uint32_t w_pitch = (uint32_t)p.K / 2, s_pitch = (uint32_t)p.groups * (SF ? 4 : 2);
+  const __amdgpu_buffer_rsrc_t w_src = make_rsrc(p.w, (uint32_t)p.N * w_pitch);
+  const __amdgpu_buffer_rsrc_t s_src = make_rsrc(p.scales, (uint32_t)p.N * s_pitch);
+  const __amdgpu_buffer_rsrc_t b_src = make_rsrc(p.biases, AFF ? (uint32_t)p.N * s_pitch : 0u);
+  const uint32_t w_col = (uint32_t)(k0 / 2 + 4 * kb), s_col = (uint32_t)((k0 + 8 * kb) / p.group) * (SF ? 4 : 2);
+  const auto load_scale = [](__amdgpu_buffer_rsrc_t src, uint32_t at) {
+    if constexpr (SF) return __builtin_amdgcn_raw_buffer_load_b32(src, (int)at, 0, 0);
+    else return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(src, (int)at, 0, 0);
+  };
+  const auto scale_value = [](uint32_t u) { return __uint_as_float(SF ? u : u << 16); };
   const RowMatrix<T> d_out(p.d_out, p.M, p.N);
+  int d_row[kRows];                    // rows past the last one repeat it
+  const T* d_at[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    d_row[i] = min(m0 + tid / kChunks + kSpan * i, p.M - 1);
+    d_at[i] = d_out.data + (size_t)d_row[i] * p.N + (tid % kChunks) * kVec;
+  }
 
+  // A step as loaded: nothing is done with a value before it is staged, so that
+  // no load is waited for here.
   struct Fetched {
     v4u d[kRows];
-    uint32_t w[kWords];
-    float s[kWords], b[kWords];
+    uint32_t w[kWords], s[kWords], b[kWords];
   };
-  auto fetch = [&](int step, Fetched& f) {
-    const int n0 = step * kStep;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int row = tid / kChunks + 32 * i, m = min(m0 + row, p.M - 1);      // rows past the last one repeat it
-      if (BM >= 32 || row < BM)
-        f.d[i] = d_out.chunk(m, n0 + (tid % kChunks) * kVec);
-    }
+  auto fetch_weights = [&](int n0, Fetched& f) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      const int n = n0 + nq * kWords + i;
-      const bool in = n < p.N;
-      const size_t row = (size_t)(in ? n : p.N - 1);
-      f.w[i] = w_at[row * pitch];
-      f.s[i] = load_scale<SF>(p.scales, row * p.groups + group);
-      f.b[i] = AFF ? load_scale<SF>(p.biases, row * p.groups + group) : -8.0f * f.s[i];
-      f.s[i] = in ? f.s[i] : 0.0f;
-      f.b[i] = in ? f.b[i] : 0.0f;
+      const uint32_t n = (uint32_t)(n0 + nq * kWords + i);
+      const bool in = col_in && n < (uint32_t)p.N;
+      const uint32_t w_off = in ? n * w_pitch + w_col : kOffNone, s_off = in ? n * s_pitch + s_col : kOffNone;
+      f.w[i] = __builtin_amdgcn_raw_buffer_load_b32(w_src, (int)w_off, 0, 0);
+      f.s[i] = load_scale(s_src, s_off);
+      if constexpr (AFF) f.b[i] = load_scale(b_src, s_off);
     }
+  };
+  auto fetch = [&](int step, Fetched& f) {             // a step whose rows are all there
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) __builtin_memcpy(&f.d[i], d_at[i] + step * kStep, 16);
+    fetch_weights(step * kStep, f);
+  };
+  auto fetch_end = [&](int step, Fetched& f) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) f.d[i] = d_out.chunk(d_row[i], step * kStep + (tid % kChunks) * kVec);
+    fetch_weights(step * kStep, f);
   };
   auto stage = [&](int buf, const Fetched& f) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int row = tid / kChunks + 32 * i;
-      if (BM >= 32 || row < BM) s_d[buf][place(row, tid % kChunks)] = f.d[i];
+      const int row = tid / kChunks + kSpan * i;
+      if (BM >= kSpan || row < BM) s_d[buf][place(row, tid % kChunks)] = f.d[i];
+    }
+    uint32_t half[kWords][2];            // the even and the odd columns' nibbles, a byte each
+    float scale[kWords], off[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      half[i][0] = f.w[i] & 0x0F0F0F0Fu;
+      half[i][1] = (f.w[i] >> 4) & 0x0F0F0F0Fu;
+      scale[i] = scale_value(f.s[i]);
+      off[i] = AFF ? scale_value(f.b[i]) : -8.0f * scale[i];
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -112,29 +138,23 @@ __global__ __launch_bounds__(kThreads) void linear_back_kernel(LinearBackParams 
       float v[kWords];
 #pragma unroll
       for (int i = 0; i < kWords; ++i)
-        v[i] = __builtin_fmaf((float)((f.w[i] >> (4 * j)) & 15u), f.s[i], f.b[i]);
-      v2u r;
-      if constexpr (sizeof(T) == 2) {
-        const v2f lo = {v[0], v[1]}, hi = {v[2 % kWords], v[3 % kWords]};
-        r.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(lo, v2bf));
-        r.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, v2bf));
-      } else {
-        r.x = __float_as_uint(v[0]);
-        r.y = __float_as_uint(v[1]);
+        v[i] = __builtin_fmaf((float)((half[i][j & 1] >> (8 * (j >> 1))) & 0xFFu), scale[i], off[i]);
+      T r[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(T) == 2) r[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
+        else r[i] = v[i];
       }
       const int row = 8 * kb + j;
-      reinterpret_cast<v2u*>(&s_w[buf][place(row, nq >> 1)])[nq & 1] = r;
+      uint8_t* const to = reinterpret_cast<uint8_t*>(&s_w[buf][place(row, chunk)]) + sub * (kWords * sizeof(T));
+      __builtin_memcpy(__builtin_assume_aligned(to, kWords * sizeof(T)), r, sizeof(r));
     }
   };
 
   v4f acc[KT][MT] = {};
-  Fetched next;
-  if (begin < end) fetch(begin, next);
-  for (int step = begin; step < end; ++step) {
-    const int buf = (step - begin) & 1;
-    stage(buf, next);
-    __syncthreads();
-    if (step + 1 < end) fetch(step + 1, next);
+  // One barrier a step: a wave writes buffer 1 - buf only after every wave has
+  // passed this step's barrier, and so has read it in the step before.
+  auto multiply_step = [&](int buf) {
 #pragma unroll
     for (int h = 0; h < kChunks / 4; ++h) {
       v4u a[KT], b[MT];
@@ -148,8 +168,29 @@ __global__ __launch_bounds__(kThreads) void linear_back_kernel(LinearBackParams 
 #pragma unroll
         for (int u = 0; u < MT; ++u) acc[t][u] = multiply<T>(a[t], b[u], acc[t][u]);
     }
-    // one barrier a step: a wave writes buffer 1 - buf only after every wave has passed this
-    // step's barrier, and so has read it in the step before
+  };
+  const int whole = min(end, p.N / kStep);             // past it at most one step, the rows' end
+  Fetched ring[2];
+  if (begin < whole) {
+    fetch(begin, ring[0]);
+    if (AHEAD == 2) fetch(min(begin + 1, whole - 1), ring[1]);
+  }
+  for (int step = begin; step < whole; step += 2) {
+#pragma unroll
+    for (int buf = 0; buf < 2; ++buf) {
+      if (step + buf >= whole) break;
+      stage(buf, ring[AHEAD == 2 ? buf : 0]);
+      __syncthreads();
+      fetch(min(step + buf + AHEAD, whole - 1), ring[AHEAD == 2 ? buf : 0]);
+      multiply_step(buf);
+    }
+  }
+  if (whole < end) {
+    const int buf = whole > begin ? (whole - begin) & 1 : 0;
+    fetch_end(end - 1, ring[0]);
+    stage(buf, ring[0]);
+    __syncthreads();
+    multiply_step(buf);
   }
 #pragma unroll
   for (int u = 0; u < MT; ++u) {
@@ -175,9 +216,9 @@ __global__ __launch_bounds__(kThreads) void linear_back_kernel(LinearBackParams 
 
 // Adds up the parts of n, in order.
 template <class T>
-__global__ __launch_bounds__(kThreads) void linear_back_join_kernel(LinearBackParams p, int splits) {
+__global__ __launch_bounds__(kJoinThreads) void linear_back_join_kernel(LinearBackParams p, int splits) {
   const size_t all = (size_t)p.M * p.K / 4;
-  const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
+  const size_t i = (size_t)blockIdx.x * kJoinThreads + threadIdx.x;
   if (i >= all) return;
   const v4f* const at = reinterpret_cast<const v4f*>(p.partials) + i;
   v4f v = at[0];
@@ -192,38 +233,39 @@ __global__ __launch_bounds__(kThreads) void linear_back_join_kernel(LinearBackPa
   }
 }
 
-int tile_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
-
-template <class T, int BM, int WM>
+template <class T, int BM, int COLS, int WAVES, int WM, int AHEAD>
 const void* pick(const LinearBackParams& p) {
   if (p.biases)
-    return p.scale_f32 ? reinterpret_cast<const void*>(&linear_back_kernel<T, BM, WM, true, true>)
-                       : reinterpret_cast<const void*>(&linear_back_kernel<T, BM, WM, true, false>);
-  return p.scale_f32 ? reinterpret_cast<const void*>(&linear_back_kernel<T, BM, WM, false, true>)
-                     : reinterpret_cast<const void*>(&linear_back_kernel<T, BM, WM, false, false>);
+    return p.scale_f32 ? reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, AHEAD, true, true>)
+                       : reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, AHEAD, true, false>);
+  return p.scale_f32 ? reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, AHEAD, false, true>)
+                     : reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, AHEAD, false, false>);
 }
 
 template <class T>
 hipError_t run(const LinearBackParams& p, hipStream_t stream) {
-  const int bm = tile_rows(p.M);
-  const void* kernel = bm == 16   ? pick<T, 16, 1>(p)
-                       : bm == 32 ? pick<T, 32, 1>(p)
-                       : bm == 64 ? pick<T, 64, 2>(p)
-                                  : pick<T, 128, 2>(p);
-  const int tiles_k = (p.K + kCols - 1) / kCols, tiles_m = (p.M + bm - 1) / bm;
-  const int steps = (p.N * (int)sizeof(T) + 127) / 128;
-  int splits = kFill / (tiles_k * tiles_m);
+  constexpr int kCols = 128;
+  const auto tiles_of = [&](int rows) { return ((p.M + rows - 1) / rows) * ((p.K + kCols - 1) / kCols); };
+  int bm = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  if (p.M > 128 && tiles_of(256) >= kLarge) bm = 256;
+  const void* kernel = bm == 16    ? pick<T, 16, kCols, 4, 1, 2>(p)
+                       : bm == 32  ? pick<T, 32, kCols, 4, 1, 2>(p)
+                       : bm == 64  ? pick<T, 64, kCols, 4, 2, 2>(p)
+                       : bm == 128 ? pick<T, 128, kCols, 4, 2, 2>(p)
+                                   : pick<T, 256, kCols, 8, 4, 2>(p);
+  const int tiles = tiles_of(bm), steps = (p.N * (int)sizeof(T) + 127) / 128;
+  int splits = kFill / tiles;
   splits = splits > kMaxSplits ? kMaxSplits : splits;
   splits = splits > steps ? steps : splits;
-  splits = splits < 1 ? 1 : splits;
+  splits = splits < 1 || bm == 256 ? 1 : splits;
   LinearBackParams q = p;
   void* args[] = {&q, &splits};
-  const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)tiles_k, (unsigned)tiles_m, (unsigned)splits),
-                                       dim3(kThreads), args, 0, stream);
+  const dim3 grid((unsigned)((p.K + kCols - 1) / kCols), (unsigned)((p.M + bm - 1) / bm), (unsigned)splits);
+  const hipError_t e = hipLaunchKernel(kernel, grid, dim3(bm == 256 ? 512 : 256), args, 0, stream);
   if (e != hipSuccess || splits == 1) return e;
   const size_t all = (size_t)p.M * p.K / 4;
   return hipLaunchKernel(reinterpret_cast<const void*>(&linear_back_join_kernel<T>),
-                         dim3((unsigned)((all + kThreads - 1) / kThreads)), dim3(kThreads), args, 0, stream);
+                         dim3((unsigned)((all + kJoinThreads - 1) / kJoinThreads)), dim3(kJoinThreads), args, 0, stream);
 }
 
 }  // namespace
@@ -231,7 +273,7 @@ hipError_t run(const LinearBackParams& p, hipStream_t stream) {
 // Room for the parts of n: there are at most kMaxSplits, and more than one only
 // while all work-groups together are no more than kFill.
 size_t linear_back_partial_bytes(int64_t M, int64_t K) {
-  const size_t parts = (size_t)M * (size_t)K * 4 * kMaxSplits, most = (size_t)kFill * 128 * kCols * 4;
+  const size_t parts = (size_t)M * (size_t)K * 4 * kMaxSplits, most = (size_t)kFill * 128 * 128 * 4;
   return ((parts < most ? parts : most) + 255) / 256 * 256;
 }
 
