@@ -24,7 +24,7 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 constexpr int kChunks = 8;           // 16-byte chunks of a tile's row
 constexpr int kJoinThreads = 256;
-constexpr int kLarge = 200;          // tiles of 256 tokens from which on they are taken
+constexpr int kCus = 256;
 constexpr int kMaxSplits = 16;       // parts of n that work-groups share
 constexpr int kFill = 512;           // work-groups that fill the device: no more parts than give so many
 
@@ -45,9 +45,18 @@ __device__ __forceinline__ v4f multiply(const v4u a, const v4u b, v4f c) {
   }
 }
 
+template <bool FIRST, class A, class B>
+struct Pick {
+  typedef A type;
+};
+template <class A, class B>
+struct Pick<false, A, B> {
+  typedef B type;
+};
+
 // T: the type of d_out as stored (uint16_t: bf16).  BM tokens by COLS columns, by
-// WAVES waves, WM of them along the tokens; AHEAD steps on their way.
-template <class T, int BM, int COLS, int WAVES, int WM, int AHEAD, bool AFF, bool SF>
+// WAVES waves, WM of them along the tokens.
+template <class T, int BM, int COLS, int WAVES, int WM, bool AFF, bool SF>
 __global__ __launch_bounds__(64 * WAVES, 2) void linear_back_kernel(LinearBackParams p, int splits) {
   constexpr int kThreads = 64 * WAVES, kCols = COLS;
   constexpr int kVec = 16 / sizeof(T), kStep = kChunks * kVec;
@@ -57,7 +66,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_back_kernel(LinearBackPa
   constexpr int kSpan = kThreads / kChunks;                        // token rows that the threads load at a time
   constexpr int kRows = BM / kSpan ? BM / kSpan : 1;               // token chunks of a thread
   static_assert(kWords == 1 || kWords == 2 || kWords == 4, "a thread's weights at a column are written at once");
-  __shared__ v4u s_d[2][BM * kChunks], s_w[2][kCols * kChunks];
+  // two buffers, apart so that a store to one may pass a load from the other
+  __shared__ v4u s_d0[BM * kChunks], s_d1[BM * kChunks], s_w0[kCols * kChunks], s_w1[kCols * kChunks];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wk = wave / WM;
@@ -81,13 +91,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_back_kernel(LinearBackPa
   };
   const auto scale_value = [](uint32_t u) { return __uint_as_float(SF ? u : u << 16); };
   const RowMatrix<T> d_out(p.d_out, p.M, p.N);
-  int d_row[kRows];                    // rows past the last one repeat it
-  const T* d_at[kRows];
+  // Where a thread's token rows start, from the tile's first on (32 bits at 256
+  // tokens, for the registers: the host keeps N below 2^22 there).  Rows past the
+  // last one repeat it.
+  using Offset = typename Pick<BM == 256, uint32_t, size_t>::type;
+  const T* const d_tile = d_out.data + (size_t)m0 * p.N;
+  const auto d_row = [&](int i) { return min(tid / kChunks + kSpan * i, p.M - 1 - m0); };
+  Offset d_at[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    d_row[i] = min(m0 + tid / kChunks + kSpan * i, p.M - 1);
-    d_at[i] = d_out.data + (size_t)d_row[i] * p.N + (tid % kChunks) * kVec;
-  }
+  for (int i = 0; i < kRows; ++i) d_at[i] = (Offset)d_row(i) * (Offset)p.N + (Offset)((tid % kChunks) * kVec);
 
   // A step as loaded: nothing is done with a value before it is staged, so that
   // no load is waited for here.
@@ -108,19 +120,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_back_kernel(LinearBackPa
   };
   auto fetch = [&](int step, Fetched& f) {             // a step whose rows are all there
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) __builtin_memcpy(&f.d[i], d_at[i] + step * kStep, 16);
+    for (int i = 0; i < kRows; ++i) __builtin_memcpy(&f.d[i], d_tile + step * kStep + d_at[i], 16);
     fetch_weights(step * kStep, f);
   };
   auto fetch_end = [&](int step, Fetched& f) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) f.d[i] = d_out.chunk(d_row[i], step * kStep + (tid % kChunks) * kVec);
+    for (int i = 0; i < kRows; ++i) f.d[i] = d_out.chunk(m0 + d_row(i), step * kStep + (tid % kChunks) * kVec);
     fetch_weights(step * kStep, f);
   };
   auto stage = [&](int buf, const Fetched& f) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int row = tid / kChunks + kSpan * i;
-      if (BM >= kSpan || row < BM) s_d[buf][place(row, tid % kChunks)] = f.d[i];
+      if (BM >= kSpan || row < BM) (buf ? s_d1 : s_d0)[place(row, tid % kChunks)] = f.d[i];
     }
     uint32_t half[kWords][2];            // the even and the odd columns' nibbles, a byte each
     float scale[kWords], off[kWords];
@@ -146,69 +158,82 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_back_kernel(LinearBackPa
         else r[i] = v[i];
       }
       const int row = 8 * kb + j;
-      uint8_t* const to = reinterpret_cast<uint8_t*>(&s_w[buf][place(row, chunk)]) + sub * (kWords * sizeof(T));
+      uint8_t* const to = reinterpret_cast<uint8_t*>(&(buf ? s_w1 : s_w0)[place(row, chunk)]) + sub * (kWords * sizeof(T));
       __builtin_memcpy(__builtin_assume_aligned(to, kWords * sizeof(T)), r, sizeof(r));
     }
   };
 
   v4f acc[KT][MT] = {};
-  // One barrier a step: a wave writes buffer 1 - buf only after every wave has
-  // passed this step's barrier, and so has read it in the step before.
-  auto multiply_step = [&](int buf) {
-#pragma unroll
-    for (int h = 0; h < kChunks / 4; ++h) {
-      v4u a[KT], b[MT];
-      const int c = 4 * h + (lane >> 4);
-#pragma unroll
-      for (int t = 0; t < KT; ++t) a[t] = s_w[buf][place(wk * (16 * KT) + 16 * t + (lane & 15), c)];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) b[t] = s_d[buf][place(wm * (16 * MT) + 16 * t + (lane & 15), c)];
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u) acc[t][u] = multiply<T>(a[t], b[u], acc[t][u]);
-    }
+  // Operation t of a wave takes the rows first + TILES l + t: their chunk's place
+  // is that of t = 0 with bits of t turned over (see place), so that one register
+  // holds all addresses.  It is hidden from the compiler, which would keep each.
+  const auto operand = [&](const v4u* tile, uint32_t at, int t, int h) {
+    return *reinterpret_cast<const v4u*>(reinterpret_cast<const uint8_t*>(tile) + (at ^ (16u * (uint32_t)(t ^ (4 * h)))) +
+                                         16 * kChunks * t);
   };
+  uint32_t w_read = 16u * (uint32_t)place(wk * (16 * KT) + KT * (lane & 15), lane >> 4);
+  uint32_t d_read = 16u * (uint32_t)place(wm * (16 * MT) + MT * (lane & 15), lane >> 4);
+  auto multiply_half = [&](int buf, int h) {
+    asm("" : "+v"(w_read), "+v"(d_read));
+    v4u a[KT], b[MT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) a[t] = operand(buf ? s_w1 : s_w0, w_read, t, h);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) b[t] = operand(buf ? s_d1 : s_d0, d_read, t, h);
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int u = 0; u < MT; ++u) acc[t][u] = multiply<T>(a[t], b[u], acc[t][u]);
+  };
+  // A step is staged in the middle of the one before it, while its operations
+  // run, and the one after it fetched into the same registers.  One barrier a
+  // step: past it every wave has read the buffer that is written next.
   const int whole = min(end, p.N / kStep);             // past it at most one step, the rows' end
-  Fetched ring[2];
-  if (begin < whole) {
-    fetch(begin, ring[0]);
-    if (AHEAD == 2) fetch(min(begin + 1, whole - 1), ring[1]);
-  }
-  for (int step = begin; step < whole; step += 2) {
+  const auto fetch_any = [&](int step, Fetched& f) {
+    if (step < whole) fetch(step, f);
+    else if (step < end) fetch_end(step, f);
+  };
+  Fetched next;
+  fetch_any(begin, next);
+  stage(0, next);
+  fetch_any(begin + 1, next);
+  __syncthreads();
+  for (int step = begin; step < end; step += 2) {
 #pragma unroll
     for (int buf = 0; buf < 2; ++buf) {
-      if (step + buf >= whole) break;
-      stage(buf, ring[AHEAD == 2 ? buf : 0]);
+      if (step + buf >= end) break;
+      multiply_half(buf, 0);
+      stage(1 - buf, next);
+      if (step + buf + 2 < whole) fetch(step + buf + 2, next);
+      else if (step + buf + 2 < end) fetch_end(step + buf + 2, next);
+      multiply_half(buf, 1);
       __syncthreads();
-      fetch(min(step + buf + AHEAD, whole - 1), ring[AHEAD == 2 ? buf : 0]);
-      multiply_step(buf);
     }
   }
-  if (whole < end) {
-    const int buf = whole > begin ? (whole - begin) & 1 : 0;
-    fetch_end(end - 1, ring[0]);
-    stage(buf, ring[0]);
-    __syncthreads();
-    multiply_step(buf);
-  }
+  // acc[t][u][i]: column KT (4 (lane / 16) + i) + t of token MT (lane % 16) + u
 #pragma unroll
   for (int u = 0; u < MT; ++u) {
-    const int m = m0 + wm * (16 * MT) + 16 * u + (lane & 15);
+    const int m = m0 + wm * (16 * MT) + MT * (lane & 15) + u;
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      const int k = k0 + wk * (16 * KT) + 16 * t + 4 * (lane >> 4);
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + wk * (16 * KT) + KT * (4 * (lane >> 4) + i);
+      float v[KT];
+#pragma unroll
+      for (int t = 0; t < KT; ++t) v[t] = acc[t][u][i];
       if (m >= p.M || k >= p.K) continue;
-      const v4f v = acc[t][u];
+      const size_t at = (size_t)m * p.K + k;
       if (splits > 1) {
-        *reinterpret_cast<v4f*>(p.partials + ((size_t)blockIdx.z * p.M + m) * p.K + k) = v;
-      } else if constexpr (sizeof(T) == 2) {
-        const v2f lo = {v[0], v[1]}, hi = {v[2], v[3]};
-        const v2u r = {__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, v2bf)),
-                       __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, v2bf))};
-        *reinterpret_cast<v2u*>(static_cast<uint16_t*>(p.d_x) + (size_t)m * p.K + k) = r;
+        float* const to = p.partials + (size_t)blockIdx.z * p.M * p.K + at;
+        __builtin_memcpy(__builtin_assume_aligned(to, 4 * (KT < 4 ? KT : 4)), v, sizeof(v));
       } else {
-        *reinterpret_cast<v4f*>(static_cast<float*>(p.d_x) + (size_t)m * p.K + k) = v;
+        T r[KT];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          if constexpr (sizeof(T) == 2) r[t] = __builtin_bit_cast(uint16_t, (__bf16)v[t]);
+          else r[t] = v[t];
+        }
+        constexpr int kBytes = KT * (int)sizeof(T);
+        __builtin_memcpy(__builtin_assume_aligned(static_cast<T*>(p.d_x) + at, kBytes < 16 ? kBytes : 16), r, sizeof(r));
       }
     }
   }
@@ -233,35 +258,61 @@ __global__ __launch_bounds__(kJoinThreads) void linear_back_join_kernel(LinearBa
   }
 }
 
-template <class T, int BM, int COLS, int WAVES, int WM, int AHEAD>
+template <class T, int BM, int COLS, int WAVES, int WM>
 const void* pick(const LinearBackParams& p) {
   if (p.biases)
-    return p.scale_f32 ? reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, AHEAD, true, true>)
-                       : reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, AHEAD, true, false>);
-  return p.scale_f32 ? reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, AHEAD, false, true>)
-                     : reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, AHEAD, false, false>);
+    return p.scale_f32 ? reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, true, true>)
+                       : reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, true, false>);
+  return p.scale_f32 ? reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, false, true>)
+                     : reinterpret_cast<const void*>(&linear_back_kernel<T, BM, COLS, WAVES, WM, false, false>);
+}
+
+// Parts of n for `tiles` work-groups of `steps` steps each: as many as give the
+// least time, a step of all CUs taking 2 us (measured: 4096 tokens through 14336 x
+// 7168) and the parts' way to memory and back 4 bytes a ps.
+int large_splits(const LinearBackParams& p, int tiles, int steps) {
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= kMaxSplits && (s == 1 || (s * tiles <= kFill && 4 * s <= steps)); ++s) {
+    const int rounds = (s * tiles + kCus - 1) / kCus;
+    const double parts = s > 1 ? 3.0 + (2 * s + 1) * (double)p.M * p.K * 4e-6 / 4.0 : 0.0;
+    const double us = rounds * ((steps + s - 1) / s) * 2.0 + parts;
+    if (s == 1 || us < least) {
+      best = s;
+      least = us;
+    }
+  }
+  return best;
 }
 
 template <class T>
 hipError_t run(const LinearBackParams& p, hipStream_t stream) {
-  constexpr int kCols = 128;
-  const auto tiles_of = [&](int rows) { return ((p.M + rows - 1) / rows) * ((p.K + kCols - 1) / kCols); };
-  int bm = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  if (p.M > 128 && tiles_of(256) >= kLarge) bm = 256;
-  const void* kernel = bm == 16    ? pick<T, 16, kCols, 4, 1, 2>(p)
-                       : bm == 32  ? pick<T, 32, kCols, 4, 1, 2>(p)
-                       : bm == 64  ? pick<T, 64, kCols, 4, 2, 2>(p)
-                       : bm == 128 ? pick<T, 128, kCols, 4, 2, 2>(p)
-                                   : pick<T, 256, kCols, 8, 4, 2>(p);
-  const int tiles = tiles_of(bm), steps = (p.N * (int)sizeof(T) + 127) / 128;
-  int splits = kFill / tiles;
-  splits = splits > kMaxSplits ? kMaxSplits : splits;
-  splits = splits > steps ? steps : splits;
-  splits = splits < 1 || bm == 256 ? 1 : splits;
+  int bm = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128, cols = 128;
+  const void* kernel = bm == 16   ? pick<T, 16, 128, 4, 1>(p)
+                       : bm == 32 ? pick<T, 32, 128, 4, 1>(p)
+                       : bm == 64 ? pick<T, 64, 128, 4, 2>(p)
+                                  : pick<T, 128, 128, 4, 2>(p);
+  if constexpr (sizeof(T) == 2) {
+    if (p.M > 128 && p.N < (1 << 22)) {
+      bm = cols = 256;
+      kernel = pick<T, 256, 256, 8, 2>(p);
+    }
+  }
+  const int tiles_k = (p.K + cols - 1) / cols, tiles_m = (p.M + bm - 1) / bm, tiles = tiles_k * tiles_m;
+  const int steps = (int)(((int64_t)p.N * (int)sizeof(T) + 127) / 128);
+  int splits;
+  if (bm == 256) {
+    splits = large_splits(p, tiles, steps);
+  } else {
+    splits = kFill / tiles;
+    splits = splits > kMaxSplits ? kMaxSplits : splits;
+    splits = splits > steps ? steps : splits;
+    splits = splits < 1 ? 1 : splits;
+  }
   LinearBackParams q = p;
   void* args[] = {&q, &splits};
-  const dim3 grid((unsigned)((p.K + kCols - 1) / kCols), (unsigned)((p.M + bm - 1) / bm), (unsigned)splits);
-  const hipError_t e = hipLaunchKernel(kernel, grid, dim3(bm == 256 ? 512 : 256), args, 0, stream);
+  const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)tiles_k, (unsigned)tiles_m, (unsigned)splits),
+                                       dim3(bm == 256 ? 512 : 256), args, 0, stream);
   if (e != hipSuccess || splits == 1) return e;
   const size_t all = (size_t)p.M * p.K / 4;
   return hipLaunchKernel(reinterpret_cast<const void*>(&linear_back_join_kernel<T>),
@@ -271,9 +322,9 @@ hipError_t run(const LinearBackParams& p, hipStream_t stream) {
 }  // namespace
 
 // Room for the parts of n: there are at most kMaxSplits, and more than one only
-// while all work-groups together are no more than kFill.
+// while all work-groups together are no more than kFill, of 256 x 256 at most.
 size_t linear_back_partial_bytes(int64_t M, int64_t K) {
-  const size_t parts = (size_t)M * (size_t)K * 4 * kMaxSplits, most = (size_t)kFill * 128 * 128 * 4;
+  const size_t parts = (size_t)M * (size_t)K * 4 * kMaxSplits, most = (size_t)kFill * 256 * 256 * 4;
   return ((parts < most ? parts : most) + 255) / 256 * 256;
 }
 
