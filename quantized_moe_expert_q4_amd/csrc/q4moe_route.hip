@@ -241,7 +241,7 @@ struct GroupOf {
 };
 
 // The token's kept groups as a mask: the top_groups highest of the keys rank[0
-// .. groups), ties to the lowest index, of those that have an expert to choose.
+// .. groups) (0 from there to a multiple of four), ties to the lowest index, of those that have an expert to choose.
 // Each lane ranks the groups l, l + L, ..: a key's place is the number of keys
 // before it.  Sets `close` where F32 (keys of 32 bits, `watch`) cannot tell the
 // last one kept from the first one left out; the order within has no effect.
@@ -250,12 +250,18 @@ __device__ __forceinline__ uint64_t keep_groups(const Key* rank, int groups, int
                                                 bool& close) {
   uint64_t mask = 0;
   Key last = 0, next = 0;
+  struct __align__(16) Keys {
+    Key k[16 / sizeof(Key)];
+  };
+  constexpr int kKeys = 16 / sizeof(Key);
   for (int g = l; g < groups; g += L) {
     const Key mine = rank[g];
     int place = 0;
-    for (int j = 0; j < groups; ++j) {
-      const Key other = rank[j];
-      place += other > mine || (other == mine && j < g);
+#pragma unroll 2
+    for (int j = 0; j < groups; j += kKeys) {          // keys past the last group are 0
+      const Keys other = *reinterpret_cast<const Keys*>(rank + j);
+#pragma unroll
+      for (int k = 0; k < kKeys; ++k) place += other.k[k] > mine || (other.k[k] == mine && j + k < g);
     }
     if (mine && place < top_groups) mask |= 1ull << g;
     last = place == top_groups - 1 ? mine : last;
@@ -306,6 +312,7 @@ __device__ __forceinline__ void choose_exact(const RouteParams& p, __amdgpu_buff
       });
       if (lane == 0) rank[g] = group_key(two, p.group_top);
     }
+    if (lane < 4) rank[p.groups + lane] = 0;
     wave_sync();
     bool close;
     const uint64_t keep = keep_groups<64>(rank, p.groups, p.top_groups, lane, false, close);
@@ -354,8 +361,8 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
   __shared__ int s_pick[kWaves][G][kRouteMaxTopK];
   __shared__ int s_count[STATS ? L * VPT : 1];
   __shared__ int s_tokens;
-  __shared__ uint64_t s_rank[GROUPED ? kWaves : 1][kRouteMaxGroups];        // of the choice in double
-  __shared__ uint32_t s_rank32[GROUPED ? kWaves : 1][G][kRouteMaxGroups];
+  __shared__ __align__(16) uint64_t s_rank[GROUPED ? kWaves : 1][kRouteMaxGroups + 4];        // of the choice in double
+  __shared__ __align__(16) uint32_t s_rank32[GROUPED ? kWaves : 1][G][kRouteMaxGroups + 4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l = lane % L, group = lane / L;
@@ -388,7 +395,6 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
       // one best expert by its logit, where no bias changes that order; else by score (plus bias)
       const bool by_logit = !p.bias && p.group_top == 1;
       const int size = p.E / p.groups;
-      const GroupOf group_of(size);
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {          // the keys stand where the scores will
         const uint32_t k = order_key(by_logit ? x[v] : s[v] + bias[v]);
@@ -396,19 +402,48 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
       }
       wave_sync();
       uint32_t* const rank = s_rank32[wave][group];
-      for (int g = l; g < p.groups; g += L) {
+      // 1 << shift lanes a group, as many as there are; each starts elsewhere in
+      // its group, so that neighbours read different banks
+      int shift = 0;
+      while ((p.groups << (shift + 1)) <= L) ++shift;
+      const int own = l & ((1 << shift) - 1), steps = (size + (1 << shift) - 1) >> shift;
+      for (int g0 = 0; g0 < p.groups; g0 += L >> shift) {
+        const int g = g0 + (l >> shift);
         BestTwo<uint32_t> two = {0, 0};
-        for (int i = 0; i < size; ++i) add_key(two, __float_as_uint(score[g * size + i]));
-        rank[g] = group_key(two, p.group_top);
+        int at = g % steps;
+#pragma unroll 4
+        for (int i = 0; i < steps; ++i) {
+          const int e = (at << shift) + own;
+          const uint32_t k = __float_as_uint(score[min(g * size + e, L * VPT - 1)]);
+          add_key(two, g < p.groups && e < size ? k : 0u);
+          at = at + 1 == steps ? 0 : at + 1;
+        }
+        for (int d = 1; d < 1 << shift; d <<= 1) {
+          const uint32_t a = __shfl_xor(two.a, d), b = __shfl_xor(two.b, d);
+          add_key(two, a);
+          add_key(two, b);
+        }
+        if (own == 0 && g < p.groups) rank[g] = group_key(two, p.group_top);
       }
+      if (l < 4) rank[p.groups + l] = 0u;
       wave_sync();
       const uint64_t keep = keep_groups<L>(rank, p.groups, p.top_groups, l, !by_logit, close_groups);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        key[v] = order_key(p.bias ? s[v] + bias[v] : x[v]);
-        key[v] = on && x[v] != -__builtin_inff() && ((keep >> (group_of(v * L + l) & 63)) & 1) ? key[v] : 0u;
-        score[v * L + l] = s[v];
+      // the same lanes strike out the keys of the other groups
+      for (int g0 = 0; g0 < p.groups; g0 += L >> shift) {
+        const int g = g0 + (l >> shift);
+        if (g < p.groups && !((keep >> g) & 1))
+          for (int e = own; e < size; e += 1 << shift) score[g * size + e] = 0.0f;
       }
+      wave_sync();
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) key[v] = __float_as_uint(score[v * L + l]);
+      if (!p.bias && !by_logit) {                // ranked by scores, chosen by logits
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) key[v] = key[v] ? order_key(x[v]) : 0u;
+      }
+      wave_sync();
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) score[v * L + l] = s[v];
     } else {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
