@@ -36,7 +36,7 @@ def test_route_groups_refuses(kw, status):
 
 
 def _back(xdtype="bf16", **kw):
-    a = dict(weights=W, scales=S, d_out=X, M=1, N=4096, K=4096, group=64, d_x=OUT, workspace=WS, workspace_bytes=1 << 26,
+    a = dict(weights=W, scales=S, d_out=X, M=1, N=4096, K=4096, group=64, d_x=OUT, workspace=WS, workspace_bytes=1 << 28,
              biases=None, scale_dtype="bfloat16")
     a.update(kw)
     return q4.validate_linear_backward(xdtype=xdtype, **a), q4.last_error()
