@@ -1,8 +1,9 @@
 /*
  * q4moe.h -- C ABI of the MI355X (gfx950) Q4/Q8 expert library: gate/up +
  * SwiGLU, the down projection and the whole expert, over expert slots, and the
- * layer around them: a group-scaled 4-bit linear, the router with its balance
- * loss, and the combination of the expert outputs.
+ * layer around them: a group-scaled 4-bit linear with the gradient of its input,
+ * low-rank adapters beside it with their gradients, the router (also over groups
+ * of experts) with its balance loss, and the combination of the expert outputs.
  *
  * What is computed (diff of @mlx-bun/inference 1.0.0, page 52,
  * kernels/glm52/streamed-experts.ts, GATE_UP_SOURCE and its launch in
@@ -599,8 +600,10 @@ int q4_validate_linear_backward_f32(const void *weights, const void *scales, con
  *   out[t,:]    = base[t,:] + scales[i] * B_i hidden[t,:]
  *
  * Sums and the hidden values are F32; out is rounded once.  bf16 calls take the
- * hidden values into the second product with 16 bits (2^-16 relative at most), a
- * 256th of the output's own rounding.  A row's result takes nothing from the rows and adapters of others, whatever those
+ * hidden values into the second product with 16 bits (2^-16 relative at most, a
+ * 256th of the output's own rounding; below 2^-110 fewer).  Sums that leave the
+ * F32 range, infinities and NaN give results that are not finite, in the rows
+ * and columns they belong to.  A row's result takes nothing from the rows and adapters of others, whatever those
  * hold.  Rows of one adapter need not stand together, but are read together
  * only within 256 neighbouring rows.
  *   a, b   device, [num_adapters][R][K] and [num_adapters][N][R], 16-byte

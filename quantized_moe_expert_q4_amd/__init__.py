@@ -1,6 +1,7 @@
 """MI355X-native Q4 expert: gate/up + SwiGLU, down projection, whole expert, and
-the layer around it: group-scaled 4-bit linear, router with its balance loss,
-combination of the expert outputs.
+the layer around it: group-scaled 4-bit linear and the gradient of its input,
+low-rank adapters and their gradients, router (also over groups of experts) with
+its balance loss, combination of the expert outputs.
 
 The computation lives in hand-written HIP kernels for gfx950 behind the C ABI
 of ``include/q4moe.h`` (``libq4moe.so`` in this package directory).  This

@@ -11,17 +11,8 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-// An element as a float (bf16 is held in a uint16_t), and back.
-template <class T>
-__device__ __forceinline__ float value(T v) {
-  if constexpr (sizeof(T) == 2) return bf16_val(v);
-  else return v;
-}
-template <class T>
-__device__ __forceinline__ T rounded(float v) {
-  if constexpr (sizeof(T) == 2) return __builtin_bit_cast(uint16_t, (__bf16)v);
-  else return v;
-}
+// A float as bf16, which is held in a uint16_t.
+__device__ __forceinline__ uint16_t rounded(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
 __device__ __forceinline__ v4f multiply_bf16(const v4u a, const v4u b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);

@@ -6,12 +6,20 @@
 //
 // A work-group takes 16 rows of one adapter (of large batches 64, which read the
 // adapter a quarter as often), gathered from a window of 256 rows (group_rows),
-// so that rows of one adapter need not stand together.  Both
-// directions take long rows to R sums ("shrink") and those to long rows
-// ("expand"); the adapter's matrix runs along the sum, or across it (ACROSS, the
-// backward pass).  The R sums of the rows stay in LDS between the two; only
-// where few rows would leave the device idle are there two launches, the first
-// with several work-groups along the long sum.
+// so that rows of one adapter need not stand together.  Both directions take long
+// rows to R sums ("shrink") and those to long rows ("expand"); the adapter's matrix
+// runs along the sum, or across it (ACROSS, the backward pass).  Small calls do
+// both in one launch, with the R sums of the rows in LDS between them; where the
+// long sum has to be shared by several work-groups to fill the device there are
+// two, the second joining the parts.
+//
+// What bounds it.  Large batches: memory and the latency of their loads: 4096 rows
+// of 7168 x 4096, rank 32, in kernels of 25 + 22 us (59 MB read; 34 MB read and 34
+// written; 2.3 and 3.0 TB/s, a copy 5.1); across, 8192 rows of 4096 x 4096, rank
+// 16, in 22 + 30 (3.1 and 4.4).  Results stored past the caches, whole lines each:
+// the two expanding kernels took 26 and 37 before.  Small calls: latency, a call of
+// one row takes 10 us and one of 64 rows of 24 adapters 16, where calls whose
+// kernels do nothing take 7.5 (one launch) and 10.3 (two).
 //
 // Matrix operations take the adapter as rows and 16 tokens as columns.  bf16:
 // the values between the products enter the second as two bf16 parts (16 bits).
@@ -26,7 +34,10 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kWindow = 256;         // rows whose adapters a work-group looks at
 constexpr int kTile = 16;            // rows of a matrix operation
 constexpr int kMaxSplits = 16;       // parts of a long sum
-constexpr int kLargeBatch = 1024;    // rows from which on a work-group takes 64
+// Rows from which on a work-group takes 64: 4096 rows of 7168 x 4096, rank 32, took
+// 75 us against 91 with 16 (before the later steps), 333 float rows of 4104 x 6147
+// 27 against 18.
+constexpr int kLargeBatch = 1024;
 constexpr int kFill = 512;           // work-groups that fill the device: no more parts than give so many
 
 // The rows of one work-group: `count` of them, all of `adapter` (-1: none);
@@ -511,8 +522,8 @@ __device__ __forceinline__ void expand_rows(const RowsParams& p, const T* w, boo
           uint16_t r[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            r[e] = rounded<uint16_t>((e < 4 ? v[e % 4] : u[e % 4]) +
-                                     __uint_as_float(e & 1 ? b[e / 2] & 0xFFFF0000u : b[e / 2] << 16));
+            r[e] = rounded((e < 4 ? v[e % 4] : u[e % 4]) +
+                           __uint_as_float(e & 1 ? b[e / 2] & 0xFFFF0000u : b[e / 2] << 16));
           put<uint16_t>(p, row_of(t, k), o, r);
         } else {
           const v4f sum = v + __builtin_bit_cast(v4f, base[t][k]);
@@ -663,6 +674,10 @@ hipError_t launch_rows(RowsParams p, bool f32, bool across, hipStream_t stream) 
   const int tiles = (p.M + kTile - 1) / kTile;
   const int slices = slices_for(p, tiles, kFill / 2, p.slice);
   p.splits = splits_for(p, tiles, kFill);
+  // One launch while a work-group reads an adapter's matrix sooner than a second
+  // launch starts: one row, rank 16, of 4096 x 4096 (128 KB) 8.5 us against 10.3
+  // with two; 64 rows, rank 32, of 7168 (448 KB) 24.1 against 21.8, 333 float rows,
+  // rank 24, of 4104 (384 KB) 40 against 19.
   const size_t table = (size_t)p.R * p.C * (f32 ? 4 : 2);
   if (p.splits == 1 || table <= (1u << 18)) return launch<kBoth, 1>(p, slices, f32, across, stream);
   const hipError_t e = launch<kShrink, 1>(p, p.splits, f32, across, stream);

@@ -1,13 +1,24 @@
 // Gradient of the input of the linear with 4-bit weights and group scales:
 // d_x[m][k] = sum_n d_out[m][n] W[n][k].
 //
-// A work-group computes BM tokens by 128 columns k.  A step covers 128 bytes of
-// the tokens' rows (64 values n in bf16, 32 in float); tokens and weights of the
-// next step are fetched into registers while one is multiplied.  Weights run
-// along k in memory and along n in the product, so a thread unpacks the words of
-// neighbouring rows n at one place k and writes them side by side: a tile in LDS
-// is [row][8 chunks of 16 bytes], tokens and columns alike, and a matrix operand
-// is one 16-byte read.
+// A work-group computes BM tokens by COLS columns k.  A step covers 128 bytes of
+// the tokens' rows (64 values n in bf16, 32 in float).  Weights run along k in
+// memory and along n in the product, so a thread unpacks the words of neighbouring
+// rows n at one place k and writes them side by side: a tile in LDS is [row][8
+// chunks of 16 bytes], tokens and columns alike, and a matrix operand is one
+// 16-byte read.
+//
+// bf16, more than 128 tokens: 256 x 256, eight waves of 128 x 64, which fills the
+// registers (128 of them sums).  Per step and CU the operations take 2048 cycles,
+// the LDS about as many, unpacking 960 of each SIMD's vector unit; what counts is
+// that they overlap.  4096 tokens through 14336 x 7168: 1420 us with 128 x 128 and
+// the loads' branches and conversions between the steps, 1212 without those, 1064
+// with 256 x 256, 900 with the next step staged between a step's operations (936
+// TFLOP/s; a library product of bf16 matrices reaches 1191 here, 1385 elsewhere).
+// Its 448 tiles are 1.75 rounds of the 256 CUs, so an eighth of the time is idle.
+// 64 tokens 42 us.  Float rows take F32 operations, 1024 tokens 1.87 ms (112
+// TFLOP/s; a library product of F32 matrices reaches 152); 77 tokens through 6147 x
+// 4104 take 70 us and 6 to join, a tile of 128 rows being filled to three fifths.
 #include "q4moe_device.h"
 #include "q4moe_layer.h"
 #include "q4moe_rows.h"
