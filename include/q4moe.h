@@ -603,9 +603,9 @@ int q4_validate_linear_backward_f32(const void *weights, const void *scales, con
  * hidden values into the second product with 16 bits (2^-16 relative at most, a
  * 256th of the output's own rounding; below 2^-110 fewer).  Sums that leave the
  * F32 range, infinities and NaN give results that are not finite, in the rows
- * and columns they belong to.  A row's result takes nothing from the rows and adapters of others, whatever those
- * hold.  Rows of one adapter need not stand together, but are read together
- * only within 256 neighbouring rows.
+ * and columns they belong to.  A row's result takes nothing from the rows and
+ * adapters of others, whatever those hold.  Rows of one adapter need not stand
+ * together, but are read together only within 256 neighbouring rows.
  *   a, b   device, [num_adapters][R][K] and [num_adapters][N][R], 16-byte
  *          aligned, in the type of the rows.  An adapter of lower rank is padded
  *          with zeros.

@@ -699,7 +699,8 @@ size_t adapter_workspace(int64_t M, int64_t N, int64_t K, int64_t R, int64_t n) 
 }
 
 hipError_t launch_adapter(const AdapterParams& p, hipStream_t stream) {
-  return launch_rows({p.x, p.a, p.b, p.ids, p.scales, p.base, p.out, p.hidden, p.partial, p.M, p.K, p.N, p.R, p.n, 0, 0, nullptr, nullptr},
+  return launch_rows({p.x, p.a, p.b, p.ids, p.scales, p.base, p.out, p.hidden, p.partial, p.M, p.K, p.N, p.R, p.n, 0, 0,
+                      nullptr, nullptr},
                      p.xf32, false, stream);
 }
 
