@@ -229,6 +229,11 @@ __device__ __forceinline__ uint32_t group_key(BestTwo<uint32_t> t, int top) {
   const float sum = key_value(t.a) + (top == 2 && t.b ? key_value(t.b) : 0.0f);
   return t.a ? order_key(sum < -__FLT_MAX__ ? -__FLT_MAX__ : sum) : 0u;
 }
+// The larger magnitude of those values, whose roundings the sum carries however small it is itself.
+__device__ __forceinline__ float group_magnitude(BestTwo<uint32_t> t, int top) {
+  const float a = t.a ? fabsf(key_value(t.a)) : 0.0f;
+  return top == 2 && t.b ? fmaxf(a, fabsf(key_value(t.b))) : a;
+}
 __device__ __forceinline__ uint64_t group_key(BestTwo<uint64_t> t, int top) {
   return t.a ? order_key(key_value(t.a) + (top == 2 && t.b ? key_value(t.b) : 0.0)) : 0ull;
 }
@@ -244,13 +249,14 @@ struct GroupOf {
 // The token's kept groups as a mask: the top_groups highest of the keys rank[0
 // .. groups) (0 from there to a multiple of four), ties to the lowest index, of those that have an expert to choose.
 // Each lane ranks the groups l, l + L, ..: a key's place is the number of keys
-// before it.  Sets `close` where F32 (keys of 32 bits, `watch`) cannot tell the
-// last one kept from the first one left out; the order within has no effect.
+// before it.  Sets `close` where F32 (keys of 32 bits, `watch`; `magnitude` as
+// of group_magnitude) cannot tell every group kept from every one left out; the
+// order within has no effect.
 template <int L, class Key>
-__device__ __forceinline__ uint64_t keep_groups(const Key* rank, int groups, int top_groups, int l, bool watch,
-                                                bool& close) {
+__device__ __forceinline__ uint64_t keep_groups(const Key* rank, const int* magnitude, int groups, int top_groups, int l,
+                                                bool watch, bool& close) {
   uint64_t mask = 0;
-  Key last = 0, next = 0;
+  float kept = __builtin_inff(), left = -__builtin_inff();   // the least a kept group may be, the most one left out
   struct __align__(16) Keys {
     Key k[16 / sizeof(Key)];
   };
@@ -264,19 +270,26 @@ __device__ __forceinline__ uint64_t keep_groups(const Key* rank, int groups, int
 #pragma unroll
       for (int k = 0; k < kKeys; ++k) place += other.k[k] > mine || (other.k[k] == mine && j + k < g);
     }
-    if (mine && place < top_groups) mask |= 1ull << g;
-    last = place == top_groups - 1 ? mine : last;
-    next = place == top_groups ? mine : next;
+    const bool in = mine && place < top_groups;
+    if (in) mask |= 1ull << g;
+    if constexpr (sizeof(Key) == 4) {
+      // A sum's two scores differ by less than 32 roundings (2^-19) from what
+      // they should.  Its keys with their biases a and b are rounded by half a
+      // step each and their sum once more: 2^-24 (|a| + |b| + |a + b|), at most
+      // 2^-22 times the larger of a and b, whose signs may differ; 2^-21 with
+      // the rounding of these limits.  Each group's own size counts: one of
+      // large biases may stand far from the border and belong beyond it.
+      const float sum = key_value(mine), off = 0x1p-19f + 0x1p-21f * __int_as_float(magnitude[g]);
+      if (in) kept = fminf(kept, sum - off);
+      else if (mine) left = fmaxf(left, sum + off);
+    }
   }
   mask = group_join<L>(mask, [](uint64_t a, uint64_t b) { return a | b; });
   if constexpr (sizeof(Key) == 4) {
     if (watch) {
-      last = group_max<L>(last);
-      next = group_max<L>(next);
-      // a sum of two scores differs by less than 64 roundings (2^-18) from what
-      // it should, those with biases by two half steps more
-      const float a = key_value(last);
-      close = last && next && !(a - key_value(next) > 0x1p-18f + 0x1p-21f * fabsf(a));
+      kept = -group_fmax<L>(-kept);
+      left = group_fmax<L>(left);
+      close = left >= kept && left > -__builtin_inff();
     }
   }
   return mask;
@@ -316,7 +329,7 @@ __device__ __forceinline__ void choose_exact(const RouteParams& p, __amdgpu_buff
     if (lane < 4) rank[p.groups + lane] = 0;
     wave_sync();
     bool close;
-    const uint64_t keep = keep_groups<64>(rank, p.groups, p.top_groups, lane, false, close);
+    const uint64_t keep = keep_groups<64>(rank, nullptr, p.groups, p.top_groups, lane, false, close);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       if (!p.bias) key[v] = order_key((double)x[v]);
@@ -403,6 +416,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
       }
       wave_sync();
       uint32_t* const rank = s_rank32[wave][group];
+      static_assert(kRouteMaxGroups <= kRouteMaxTopK, "the groups' magnitudes stand where the choice will");
       // 1 << shift lanes a group, as many as there are; each starts elsewhere in
       // its group, so that neighbours read different banks
       int shift = 0;
@@ -424,11 +438,14 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(RouteParams p) {
           add_key(two, a);
           add_key(two, b);
         }
-        if (own == 0 && g < p.groups) rank[g] = group_key(two, p.group_top);
+        if (own == 0 && g < p.groups) {
+          rank[g] = group_key(two, p.group_top);
+          pick[g] = __float_as_int(group_magnitude(two, p.group_top));
+        }
       }
       if (l < 4) rank[p.groups + l] = 0u;
       wave_sync();
-      const uint64_t keep = keep_groups<L>(rank, p.groups, p.top_groups, l, !by_logit, close_groups);
+      const uint64_t keep = keep_groups<L>(rank, pick, p.groups, p.top_groups, l, !by_logit, close_groups);
       // the same lanes strike out the keys of the other groups
       for (int g0 = 0; g0 < p.groups; g0 += L >> shift) {
         const int g = g0 + (l >> shift);
