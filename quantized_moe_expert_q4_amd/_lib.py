@@ -284,19 +284,37 @@ def _dtype_name(dtype) -> str:
 _XDTYPE_NAMES = {"bf16": "bfloat16", "f32": "float32"}
 
 
+def _current_device() -> int:
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _raw_device()
+
+
+_raw_device = None
+
+
 def _args(*specs) -> None:
     """Reject tensor arguments the kernels would misread.  Each spec is
     (name, tensor, dtype, numel): the tensor must have that dtype, be
-    contiguous, hold at least ``numel`` elements and live in device memory
-    (dtype, layout and size of every argument are checked before any
-    device).  Raw integer pointers pass unchecked; None is left to the
-    library's own checks (required pointers) or means "skip" (probes)."""
+    contiguous, hold at least ``numel`` elements and live in the memory of the
+    current device, where the call runs (dtype, layout and size of every
+    argument are checked before any device).  Raw integer pointers pass
+    unchecked; None is left to the library's own checks (required pointers) or
+    means "skip" (probes)."""
+    device = None
     for name, t, dtype, numel in specs:
-        if t is not None and not isinstance(t, int) and not (
-                _dtype_name(t.dtype) == dtype and t.numel() >= numel and t.is_cuda and t.is_contiguous()):
-            break
+        if t is not None and not isinstance(t, int):
+            at = t.get_device()
+            if device is None:
+                device = at
+            if not (at == device and at >= 0 and _dtype_names.get(t.dtype) == dtype and t.numel() >= numel
+                    and t.is_contiguous()):
+                break                    # a type's first call too: the checks below name it
     else:
-        return
+        if device is None or device == _current_device():
+            return
     live = [sp for sp in specs if sp[1] is not None and not isinstance(sp[1], int)]
     for name, t, dtype, numel in live:
         got = _dtype_name(t.dtype)
@@ -309,6 +327,9 @@ def _args(*specs) -> None:
     for name, t, _, _ in live:
         if t.device.type != "cuda":
             raise ValueError(f"{name} must be a device (cuda) tensor, not on {t.device.type}")
+    for name, t, _, _ in live:
+        if t.get_device() != _current_device():
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{_current_device()}")
 
 
 def _slots_spec(name: str, t, num_slots: int, stride: int, layout):
