@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import quantized_moe_expert_q4_amd as q4
-from layer_gpu_helpers import TYPES, host, i32
+from layer_gpu_helpers import TYPES, host, i32, replayed
 from test_gpu_adapter import Case
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +91,53 @@ def test_adapters_no_row_names():
     torch.cuda.synchronize()
     _, _, want = c.want_backward()[0]
     assert torch.equal(d_b.cpu().double(), torch.from_numpy(want))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K,R", [(1030, 1099, 1096, 24), (1030, 1099, 1096, 72), (70, 2503, 2504, 64), (70, 300, 264, 40)])
+def test_infinities_and_nan_stay_where_they_are(M, N, K, R, kind):
+    # the calls again with one adapter, a row of x, of base and of d_out made infinite or NaN: all else keeps its bits
+    n, bad = 5, 2
+    c = Case(M + R, M, N, K, R, n, kind)
+
+    def run():
+        o = [*c.outputs(), *c.gradients()]
+        c.forward(*o[:2])
+        c.backward(*o[2:])
+        torch.cuda.synchronize()
+        return o
+    clean = run()
+    ids = host(c.ids)
+    free = [int(np.flatnonzero(ids == i)[1]) for i in (0, 1)]           # rows of the adapters 0 and 1
+    none = int(np.flatnonzero((ids < 0) | (ids >= n))[0])
+    c.a[bad, R - 1, K - 1], c.b[bad, 0, 0] = float("nan"), float("inf")
+    c.x[free[0], 3], c.d_out[free[1], N - 1] = float("inf"), float("nan")
+    c.x[none], c.d_out[none] = float("nan"), float("inf")               # a row without an adapter
+    out, hidden, d_x, d_a, d_b = run()
+    torch.cuda.synchronize()
+    row = np.arange(M)
+    same = torch.from_numpy((ids != bad) & (row != free[0])).cuda()
+    assert torch.equal(out[same], clean[0][same]) and torch.equal(hidden[same], clean[1][same])
+    assert not torch.isfinite(hidden[free[0]]).any()
+    same = torch.from_numpy((ids != bad) & (row != free[1])).cuda()
+    assert torch.equal(d_x[same], clean[2][same])
+    assert not torch.isfinite(d_x[free[1]].float()).any()
+    for i in (3, 4):                     # the adapters without any such row
+        assert torch.equal(d_a[i], clean[3][i]) and torch.equal(d_b[i], clean[4][i])
+    assert torch.equal(d_b[0], clean[4][0])                             # x has no part in it
+    assert not torch.isfinite(d_a[0, :, 3]).any() and not torch.isfinite(d_b[1, N - 1]).any()
+
+
+@pytest.mark.parametrize("M,N,K,R", [(1030, 1099, 1096, 24), (70, 2503, 2504, 64)])
+def test_two_launches_in_a_graph(M, N, K, R):
+    c = Case(M, M, N, K, R, 3, "bf16")
+    outs = [*c.outputs(), *c.gradients()]
+
+    def both():
+        c.forward(*outs[:2])
+        c.backward(*outs[2:])
+    both()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    for got in replayed(both, outs):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
