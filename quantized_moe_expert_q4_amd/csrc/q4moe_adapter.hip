@@ -36,9 +36,13 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kWindow = 256;         // rows whose adapters a work-group looks at
 constexpr int kTile = 16;            // rows of a matrix operation
 constexpr int kMaxSplits = 16;       // parts of a long sum
-// Rows from which on a work-group takes 64: 4096 rows of 7168 x 4096, rank 32, took
-// 75 us against 91 with 16 (before the later steps), 333 float rows of 4104 x 6147
-// 27 against 18.
+// Rows from which on a work-group takes 64 of an adapter instead of 16.  Forward,
+// 7168 to 4096, eight adapters, rows of one together, bf16 rank 32: 19 us against
+// 17 with 16 rows for 512 rows, 23 against 20 for 1024, 33 against 30 for 2048, 55
+// against 62 for 4096; rank 16 18 against 31 for 512, 21 against 32 for 1024, 47
+// against 56 for 4096; float rank 32 29 against 23, 37 against 34, 104 against 135.
+// The backward call gains from 768 rows on (bf16, rank 32: 58 against 65; 63
+// against 70 for 1024, 121 against 145 for 4096).
 constexpr int kLargeBatch = 1024;
 constexpr int kFill = 512;           // work-groups that fill the device: no more parts than give so many
 
@@ -688,9 +692,13 @@ hipError_t launch_rows(RowsParams p, bool f32, bool across, hipStream_t stream) 
   const int slices = slices_for(p, tiles, kFill / 2, p.slice);
   p.splits = splits_for(p, tiles, kFill);
   // One launch while a work-group reads an adapter's matrix sooner than a second
-  // launch starts: one row, rank 16, of 4096 x 4096 (128 KB) 8.5 us against 10.3
-  // with two; 64 rows, rank 32, of 7168 (448 KB) 24.1 against 21.8, 333 float rows,
-  // rank 24, of 4104 (384 KB) 40 against 19.
+  // launch starts.  Forward to 4096 columns, three adapters, one launch against two:
+  // 24 KB (bf16, rank 8, of 1544) 8.6 us against 11.3 for one row, 8.3 against 11.0
+  // for 333; 128 KB (rank 16 of 4096) 10.1 against 12.3, 13.1 against 11.7; 224 KB
+  // (rank 16 of 7168) 13.2 against 13.0, 17.8 against 14.3; 448 KB (rank 32) 19.2
+  // against 14.5, 23.7 against 15.1.  The rule asks nothing about rows: 1000 of them
+  // are better off with two launches from 128 KB on (22 against 16; 224 KB 32
+  // against 18).
   const size_t table = (size_t)p.R * p.C * (f32 ? 4 : 2);
   if (p.splits == 1 || table <= (1u << 18)) return launch<kBoth, 1>(p, slices, f32, across, stream);
   const hipError_t e = launch<kShrink, 1>(p, p.splits, f32, across, stream);

@@ -10,8 +10,9 @@
 //
 // bf16, more than 128 tokens: 256 x 256, eight waves of 128 x 64, which fills the
 // registers (128 of them sums).  Per step and CU the operations take 2048 cycles,
-// the LDS about as many, unpacking 960 of each SIMD's vector unit; what counts is
-// that they overlap.  4096 tokens through 14336 x 7168: 1420 us with 128 x 128 and
+// the LDS as many (counters: each is busy for 37% of the kernel's time, the LDS for
+// 37% of that with conflicts, see place()), unpacking 960 of each SIMD's vector
+// unit; what counts is that they overlap.  4096 tokens through 14336 x 7168: 1420 us with 128 x 128 and
 // the loads' branches and conversions between the steps, 1212 without those, 1064
 // with 256 x 256, 900 with the next step staged between a step's operations (936
 // TFLOP/s; a library product of bf16 matrices reaches 1191 here, 1385 elsewhere).
@@ -40,8 +41,12 @@ constexpr int kMaxSplits = 16;       // parts of n that work-groups share
 constexpr int kFill = 512;           // work-groups that fill the device: no more parts than give so many
 
 // Place of a row's chunk: the eight chunks change places from row to row and
-// from eight rows to the next, so that neither the reads (16 rows of one chunk)
-// nor the weights' writes (rows eight apart) meet in a bank.
+// from eight rows to the next, so that the weights' writes (rows eight apart) do
+// not meet in a bank.  The operands' reads do: they take one chunk of 16 rows KT
+// or MT (four or eight, in the largest tile) apart, all odd or all even ones,
+// which lie in one half of the banks, so that they meet at least twice there.
+// (Tokens and columns are dealt out to the operations in that order so that a
+// lane's results are neighbours.)
 __device__ __forceinline__ int place(int row, int chunk) { return row * kChunks + (chunk ^ ((row ^ (row >> 3)) & 7)); }
 
 template <class T>
@@ -157,7 +162,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void linear_back_kernel(LinearBackPa
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       // (q - 8) s, or q s + b, rounded once (to F32, and for bf16 once more: as a
-      // bf16 matrix of these weights would hold them)
+      // bf16 matrix of these weights would hold them; two bf16 parts would take
+      // twice the operations to bring the error against 64 bits from 2.1e-3 to the
+      // 1.7e-3 of the output's own rounding)
       float v[kWords];
 #pragma unroll
       for (int i = 0; i < kWords; ++i)
