@@ -12,10 +12,11 @@
 // registers (128 of them sums).  Per step and CU the operations take 2048 cycles,
 // the LDS as many (counters: each is busy for 37% of the kernel's time, the LDS for
 // 37% of that with conflicts, see place()), unpacking 960 of each SIMD's vector
-// unit; what counts is that they overlap.  4096 tokens through 14336 x 7168: 1420 us with 128 x 128 and
-// the loads' branches and conversions between the steps, 1212 without those, 1064
-// with 256 x 256, 900 with the next step staged between a step's operations (936
-// TFLOP/s; a library product of bf16 matrices reaches 1191 here, 1385 elsewhere).
+// unit; what counts is that they overlap.  4096 tokens through 14336 x 7168: 1420
+// us with 128 x 128 and the loads' branches and conversions between the steps, 1212
+// without those, 1064 with 256 x 256, 900 with the next step staged between a
+// step's operations (936 TFLOP/s; a library product of bf16 matrices reaches 1191
+// here, 1385 elsewhere).
 // Its 448 tiles are 1.75 rounds of the 256 CUs, so an eighth of the time is idle.
 // 64 tokens 42 us.  Float rows take F32 operations, 1024 tokens 1.87 ms (112
 // TFLOP/s; a library product of F32 matrices reaches 152); 77 tokens through 6147 x
